@@ -61,7 +61,8 @@ typedef enum {
   TQ_ENOMEM = 4         /* device or host allocation failed (tq_codebook_load only) */
 } tq_status;
 
-typedef enum { TQ_F32 = 0, TQ_BF16 = 1 } tq_dtype;
+/* TQ_F16 is taken by the page-cache calls (tq_kv_pages) alone. */
+typedef enum { TQ_F32 = 0, TQ_BF16 = 1, TQ_F16 = 2 } tq_dtype;
 
 typedef enum {
   TQ_ROT_HADAMARD = 0,  /* Pi = H_d diag(sigma) / sqrt(d), applied as sign flip + FWHT */
@@ -337,6 +338,104 @@ int tq_decode_kernel_for(const tq_ctx* ctx, int hq, int hkv);
 tq_status tq_decompress(const tq_ctx* ctx, const uint8_t* k_codes, const uint8_t* k_signs,
                         const uint16_t* k_norms, const uint8_t* v_codes, const uint16_t* v_params,
                         int64_t n_vec, float* k_out, float* v_out, void* stream);
+
+/* ---------------------------------------------------------------------------------
+ * Page caches: keys and values held as ordinary 16-bit vectors or as MXFP4 records.
+ *
+ * The packed caches above hold the long past; a serving program also holds the prompt
+ * it is reading and the newest tokens of every sequence uncompressed, in pages. These
+ * calls rotate and append new tokens, read tokens back (e.g. to hand old pages to
+ * tq_compress_kv_slots), and attend over the pages with one new token per sequence or
+ * with a chunk of them. Attention over pages and over a packed cache of the same
+ * sequence's earlier tokens is combined by tq_merge_attention.
+ * ------------------------------------------------------------------------------- */
+
+/* Records of a page cache.
+ *   TQ_KV_BF16, TQ_KV_F16  d 16-bit floats
+ *   TQ_KV_MXFP4            d e2m1 codes (sign, 2 exponent bits, 1 mantissa bit: 0, 0.5, 1,
+ *                          1.5, 2, 3, 4, 6), coordinate j in nibble j % 2 (low first) of
+ *                          byte j / 2, and one E8M0 scale byte s per 32 coordinates (factor
+ *                          2^(s - 127); s = 255 marks a block that is not finite). */
+typedef enum { TQ_KV_BF16 = 0, TQ_KV_F16 = 1, TQ_KV_MXFP4 = 2 } tq_kv_format;
+
+/* A page cache: n_pages pages of page_size token records per KV head, in caller-owned
+ * device memory. Head h's record of token t of page p starts at element
+ *   p * page_stride + t * token_stride + h * head_stride
+ * of k and of v (elements: 16-bit floats, or bytes of codes), its scale bytes at the same
+ * expression in the scale strides. A record's own coordinates are contiguous.
+ *   pages_per_head  0: a page holds its tokens for every KV head (slot maps [n], block
+ *                   tables [batch][max_pages]); 1: a page belongs to one (sequence, KV
+ *                   head), as in the packed caches (slot maps [n][hkv], block tables
+ *                   [batch][hkv][max_pages]; head_stride and scale_head_stride unused)
+ *   page_size       tokens per page, 1 to 2^20; a multiple of 16 takes one block-table
+ *                   entry per tile of the attention kernels, others one per token
+ *   k, v            16-byte aligned, 16-bit strides multiples of 8, code strides of 16
+ *   k_scales, v_scales  MXFP4 only (else NULL and strides ignored): aligned to, and
+ *                   strides multiples of, d / 32 bytes
+ * The structure is read during the call only. */
+typedef struct {
+  tq_kv_format format;
+  int hkv;
+  int pages_per_head;
+  int64_t page_size;
+  int64_t n_pages;
+  void* k;
+  void* v;
+  int64_t page_stride, token_stride, head_stride;
+  uint8_t* k_scales;
+  uint8_t* v_scales;
+  int64_t scale_page_stride, scale_token_stride, scale_head_stride;
+} tq_kv_pages;
+
+/* Position rotation of a vector's first rot_dim coordinates.
+ *   cos_sin      device fp32 [n_positions][rot_dim], 16-byte aligned: the cosines of a
+ *                position's rot_dim / 2 angles, then their sines
+ *   positions    device int64 [n], 8-byte aligned: each row's position
+ *   rot_dim      a multiple of 16, at most d (other sizes: TQ_EUNSUPPORTED)
+ *   interleaved  0: angle i turns coordinates (i, i + rot_dim / 2); 1: (2i, 2i + 1)
+ * (a, b) becomes (a cos - b sin, b cos + a sin), each product and the sum rounded to fp32. */
+typedef struct {
+  const float* cos_sin;
+  const int64_t* positions;
+  int64_t n_positions;
+  int rot_dim;
+  int interleaved;
+} tq_rope;
+
+/* Append n tokens: rotate q and k (rope not NULL), write the rotated queries to q_out and
+ * the keys and values to the cache, quantised if it is MXFP4.
+ *   dtype   TQ_BF16 or TQ_F16, the type of q, k, v and q_out; a 16-bit cache holds the same
+ *           type, an MXFP4 cache takes TQ_BF16
+ *   q, k, v device rows of hq, hkv, hkv heads of d coordinates (heads contiguous), rows
+ *           q_stride, k_stride, v_stride elements apart: e.g. slices of one projection's
+ *           output. 16-byte aligned, strides multiples of 8. q (with q_out) may be NULL.
+ *   slot    device int64 [n] ([n][hkv] with pages_per_head), 8-byte aligned: the cache row
+ *           page * page_size + token of each record, distinct. -1 marks padding: the row is
+ *           skipped, its position unread and its q_out row left as it was (with
+ *           pages_per_head the slot of KV head 0 decides for q_out). Any other value
+ *           outside [0, n_pages * page_size), or a position outside [0, n_positions), sets
+ *           the context's device error word (tq_check_device returns TQ_EINVAL); such a
+ *           record, and every record of a row with such a position, is not written.
+ *   q_out   rows of hq heads, q_out_stride elements apart; may be q itself, else must not
+ *           overlap the inputs
+ * Arithmetic is fp32 with one rounding at the end. MXFP4: a block of 32 with largest
+ * magnitude a gets the scale 2^e, e = max(floor(log2 a) - 2, -126), and each coordinate
+ * x / 2^e rounded to the nearest code (ties to the even code, magnitudes above 6 become 6);
+ * a block holding an infinity or a NaN gets the scale byte 255 and reads back as NaN. */
+tq_status tq_append_kv_pages(const tq_ctx* ctx, const tq_kv_pages* pages, tq_dtype dtype, int64_t n, int hq,
+                             const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+                             int64_t v_stride, const tq_rope* rope, const int64_t* slot, void* q_out,
+                             int64_t q_out_stride, void* stream);
+
+/* Read n tokens back to dense rows, e.g. the input of tq_compress_kv_slots.
+ *   slot          as in tq_append_kv_pages (entries may repeat); a row with slot -1 is
+ *                 left as it was, a slot outside the cache sets the error word and is
+ *                 left as well
+ *   k_out, v_out  device [n][hkv][d], 16-byte aligned, of the cache's type (MXFP4: bf16,
+ *                 which holds every value up to its own largest exactly); either may be
+ *                 NULL to skip it */
+tq_status tq_read_kv_pages(const tq_ctx* ctx, const tq_kv_pages* pages, int64_t n, const int64_t* slot,
+                           void* k_out, void* v_out, void* stream);
 
 #ifdef __cplusplus
 }

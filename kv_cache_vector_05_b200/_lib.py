@@ -16,7 +16,8 @@ import numpy as np
 LIB_PATH = os.environ.get("TQ_LIBRARY") or os.path.join(os.path.dirname(os.path.abspath(__file__)), "libtq.so")
 
 TQ_OK, TQ_EINVAL, TQ_EUNSUPPORTED, TQ_ECUDA, TQ_ENOMEM = 0, 1, 2, 3, 4
-TQ_F32, TQ_BF16 = 0, 1
+TQ_F32, TQ_BF16, TQ_F16 = 0, 1, 2
+TQ_KV_BF16, TQ_KV_F16, TQ_KV_MXFP4 = 0, 1, 2
 TQ_ROT_HADAMARD, TQ_ROT_HAAR = 0, 1
 TQ_DECODE_AUTO, TQ_DECODE_TCGEN05, TQ_DECODE_MMA, TQ_DECODE_CUDA_CORE = 0, 1, 2, 3
 DECODE_KERNEL_NAMES = {TQ_DECODE_TCGEN05: "tcgen05", TQ_DECODE_MMA: "mma", TQ_DECODE_CUDA_CORE: "cuda_core"}
@@ -27,6 +28,7 @@ EXPORTED = (
     "tq_decode_workspace_bytes", "tq_decode_attention", "tq_decode_attention_paged", "tq_decompress",
     "tq_set_profile_events", "tq_check_device", "tq_decode_attention_static", "tq_decode_static_scratch_capacity",
     "tq_decode_attention_partial", "tq_merge_attention", "tq_set_decode_kernel", "tq_decode_kernel_for",
+    "tq_append_kv_pages", "tq_read_kv_pages",
 )
 
 
@@ -49,6 +51,33 @@ class tq_params(ctypes.Structure):
         ("hadamard_signs", ctypes.POINTER(ctypes.c_byte)),
         ("haar", ctypes.POINTER(ctypes.c_double)),
         ("qjl_S", ctypes.POINTER(ctypes.c_float)),
+    ]
+
+
+class tq_kv_pages(ctypes.Structure):
+    _fields_ = [
+        ("format", ctypes.c_int),
+        ("hkv", ctypes.c_int),
+        ("pages_per_head", ctypes.c_int),
+        ("page_size", ctypes.c_int64),
+        ("n_pages", ctypes.c_int64),
+        ("k", ctypes.c_void_p),
+        ("v", ctypes.c_void_p),
+        ("page_stride", ctypes.c_int64), ("token_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64),
+        ("k_scales", ctypes.c_void_p),
+        ("v_scales", ctypes.c_void_p),
+        ("scale_page_stride", ctypes.c_int64), ("scale_token_stride", ctypes.c_int64),
+        ("scale_head_stride", ctypes.c_int64),
+    ]
+
+
+class tq_rope(ctypes.Structure):
+    _fields_ = [
+        ("cos_sin", ctypes.c_void_p),
+        ("positions", ctypes.c_void_p),
+        ("n_positions", ctypes.c_int64),
+        ("rot_dim", ctypes.c_int),
+        ("interleaved", ctypes.c_int),
     ]
 
 
@@ -103,6 +132,11 @@ def _load() -> ctypes.CDLL:
     lib.tq_set_decode_kernel.restype = c_int
     lib.tq_decode_kernel_for.argtypes = [vp, c_int, c_int]
     lib.tq_decode_kernel_for.restype = c_int
+    pages, rope = ctypes.POINTER(tq_kv_pages), ctypes.POINTER(tq_rope)
+    lib.tq_append_kv_pages.argtypes = [vp, pages, c_int, i64, c_int, vp, i64, vp, i64, vp, i64, rope, vp, vp, i64, vp]
+    lib.tq_append_kv_pages.restype = c_int
+    lib.tq_read_kv_pages.argtypes = [vp, pages, i64, vp, vp, vp, vp]
+    lib.tq_read_kv_pages.restype = c_int
     return lib
 
 
@@ -157,6 +191,11 @@ def _stream(stream):
     return ctypes.c_void_p(s.cuda_stream)
 
 
+def _current_device() -> int:
+    import torch
+    return torch.cuda.current_device()
+
+
 class Context:
     """Owns a ``tq_ctx`` (codebook, rotation and QJL matrix on the device)."""
 
@@ -185,6 +224,7 @@ class Context:
             keep.append(h)
             p.haar = h.ctypes.data_as(ctypes.POINTER(ctypes.c_double))
         self.rotation = rotation
+        self.device = _current_device()
         handle = ctypes.c_void_p()
         _check(lib.tq_codebook_load(ctypes.byref(p), _stream(stream), ctypes.byref(handle)), "tq_codebook_load")
         self.handle = handle
@@ -433,3 +473,137 @@ def tq_decompress(ctx: Context, packed: dict, n_vec: int, keys: bool = True, val
                              _ptr(k_out if keys else None), _ptr(v_out if values else None),
                              _stream(stream)), "tq_decompress")
     return (k_out if keys else None), (v_out if values else None)
+
+
+# ------------------------------------------------------------------ page caches
+
+class KVPages:
+    """A page cache over caller-owned CUDA tensors (``tq_kv_pages``): `k` and `v` of shape
+    [n_pages, page_size, hkv, width], or [n_pages, page_size, width] with pages of one
+    (sequence, KV head) each; any strides with contiguous records, the same for both. width is
+    d for bfloat16 and float16 pages; uint8 pages hold MXFP4 codes (width d / 2) and need
+    `k_scales` and `v_scales` (uint8, the same leading shape, width d / 32)."""
+
+    def __init__(self, k, v, k_scales=None, v_scales=None):
+        import torch
+        formats = {torch.bfloat16: TQ_KV_BF16, torch.float16: TQ_KV_F16, torch.uint8: TQ_KV_MXFP4}
+        if k.dtype not in formats or v.dtype != k.dtype:
+            raise ValueError("pages must both be bfloat16, float16 or uint8 (MXFP4) tensors")
+        self.format = formats[k.dtype]
+        mx = self.format == TQ_KV_MXFP4
+        if (k_scales is None) == mx or (v_scales is None) == mx:
+            raise ValueError("MXFP4 pages need k_scales and v_scales, other pages take none")
+        tensors = [k, v] + ([k_scales, v_scales] if mx else [])
+        if k.dim() not in (3, 4) or any(t.shape[:-1] != k.shape[:-1] or not t.is_cuda or t.device != k.device
+                                        for t in tensors):
+            raise ValueError("pages must be CUDA tensors of one leading shape [n_pages, page_size(, hkv)]")
+        self.d = k.shape[-1] * (2 if mx else 1)
+        pairs = [(k, v)] + ([(k_scales, v_scales)] if mx else [])
+        if v.shape != k.shape or (mx and (k_scales.shape[-1] * 32 != self.d or v_scales.shape != k_scales.shape
+                                          or k_scales.dtype != torch.uint8 or v_scales.dtype != torch.uint8)):
+            raise ValueError("keys and values (and their scales, one byte per 32 coordinates) must have one shape")
+        for a, b in pairs:
+            if a.stride() != b.stride() or (a.shape[-1] > 1 and a.stride(-1) != 1):
+                raise ValueError("keys and values must have the same strides and contiguous records")
+        self.k, self.v, self.k_scales, self.v_scales = k, v, k_scales, v_scales
+        self.per_head = k.dim() == 3
+        self.hkv = None if self.per_head else k.shape[2]
+        self.n_pages, self.page_size = k.shape[0], k.shape[1]
+        self.dtype = torch.bfloat16 if mx else k.dtype        # of q, of appended and of read rows
+        self.device = k.device
+        p = tq_kv_pages()
+        p.format, p.pages_per_head = self.format, int(self.per_head)
+        p.page_size, p.n_pages = self.page_size, self.n_pages
+        p.k, p.v = k.data_ptr(), v.data_ptr()
+        p.page_stride, p.token_stride = k.stride(0), k.stride(1)
+        p.head_stride = 0 if self.per_head else k.stride(2)
+        if mx:
+            p.k_scales, p.v_scales = k_scales.data_ptr(), v_scales.data_ptr()
+            p.scale_page_stride, p.scale_token_stride = k_scales.stride(0), k_scales.stride(1)
+            p.scale_head_stride = 0 if self.per_head else k_scales.stride(2)
+        self._struct = p
+
+    def struct(self, ctx: Context, hkv: int):
+        """The C structure for `hkv` KV heads, checked against the context."""
+        if self.d != ctx.d or self.device.index != ctx.device:
+            raise ValueError("the page cache has another d or device than the context")
+        if not self.per_head and hkv != self.hkv:
+            raise ValueError(f"the page cache holds {self.hkv} KV heads, not {hkv}")
+        p = self._struct
+        if p.hkv != hkv:
+            if p.hkv:                                         # a per-head cache used with another head count
+                p = tq_kv_pages.from_buffer_copy(p)
+            p.hkv = hkv
+        return ctypes.byref(p)
+
+
+def _rows(t, what: str, n: int, d: int, pages: KVPages) -> int:
+    """Row stride of [n, heads, d] rows of the cache's 16-bit type with contiguous heads."""
+    if t.dim() != 3 or t.shape[0] != n or t.shape[2] != d or t.dtype != pages.dtype or t.device != pages.device:
+        raise ValueError(f"{what} must be [{n}, heads, {d}] of {pages.dtype} on {pages.device}")
+    if t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != d):
+        raise ValueError(f"{what} must have contiguous heads")
+    return t.stride(0) if n > 1 else t.shape[1] * d
+
+
+def _index(t, what: str, dtype, shape, pages: KVPages):
+    if t.dtype != dtype or tuple(t.shape) != shape or not t.is_contiguous() or t.device != pages.device:
+        raise ValueError(f"{what} must be a contiguous {dtype} tensor of shape {shape} on {pages.device}")
+
+
+def tq_append_kv_pages(ctx: Context, pages: KVPages, k, v, slot, q=None, q_out=None, cos_sin=None, positions=None,
+                       interleaved: bool = False, stream=None):
+    """Append the n tokens of k and v [n, hkv, d] at cache rows `slot` (int64 [n], or [n, hkv]
+    with per-head pages; -1 skips a row), after the position rotation `cos_sin` (fp32
+    [n_positions, rot_dim]) at `positions` (int64 [n]) if given; q [n, hq, d] is rotated into
+    q_out (a new tensor if None; may be q). Rows may be strided. Returns q_out."""
+    import torch
+    n, hkv = k.shape[0], k.shape[1]
+    p = pages.struct(ctx, hkv)
+    ks, vs = _rows(k, "k", n, ctx.d, pages), _rows(v, "v", n, ctx.d, pages)
+    if v.shape != k.shape:
+        raise ValueError("k and v must have one shape")
+    _index(slot, "slot", torch.int64, (n, hkv) if pages.per_head else (n,), pages)
+    hq = qs = qos = 0
+    if q is not None:
+        hq, qs = q.shape[1], _rows(q, "q", n, ctx.d, pages)
+        if q_out is None:
+            q_out = torch.empty((n, hq, ctx.d), dtype=q.dtype, device=q.device)
+        qos = _rows(q_out, "q_out", n, ctx.d, pages)
+        if q_out.shape != q.shape:
+            raise ValueError("q and q_out must have one shape")
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    rope = None
+    if cos_sin is not None:
+        _index(positions, "positions", torch.int64, (n,), pages)
+        if cos_sin.dim() != 2:
+            raise ValueError("cos_sin must be [n_positions, rot_dim]")
+        _index(cos_sin, "cos_sin", torch.float32, tuple(cos_sin.shape), pages)
+        rope = ctypes.byref(tq_rope(cos_sin.data_ptr(), positions.data_ptr(), cos_sin.shape[0], cos_sin.shape[1],
+                                    int(interleaved)))
+    _check(lib.tq_append_kv_pages(ctx.handle, p, TQ_F16 if pages.dtype == torch.float16 else TQ_BF16, n, hq, _ptr(q),
+                                  qs, _ptr(k), ks, _ptr(v), vs, rope, _ptr(slot), _ptr(q_out), qos,
+                                  _stream(stream)), "tq_append_kv_pages")
+    return q_out
+
+
+def tq_read_kv_pages(ctx: Context, pages: KVPages, slot, hkv: int, keys: bool = True, values: bool = True,
+                     k_out=None, v_out=None, stream=None):
+    """Read the tokens at cache rows `slot` (int64 [n], or [n, hkv] with per-head pages) back to
+    dense (k, v) [n, hkv, d] of the cache's type (bfloat16 for MXFP4); rows with slot -1 are
+    left as they were. `keys` / `values` False skips that half (None is returned for it)."""
+    import torch
+    n = slot.shape[0]
+    p = pages.struct(ctx, hkv)
+    _index(slot, "slot", torch.int64, (n, hkv) if pages.per_head else (n,), pages)
+    outs = []
+    for want, t, what in ((keys, k_out, "k_out"), (values, v_out, "v_out")):
+        if want and t is None:
+            t = torch.empty((n, hkv, ctx.d), dtype=pages.dtype, device=pages.device)
+        elif want:
+            _index(t, what, pages.dtype, (n, hkv, ctx.d), pages)
+        outs.append(t if want else None)
+    _check(lib.tq_read_kv_pages(ctx.handle, p, n, _ptr(slot), _ptr(outs[0]), _ptr(outs[1]), _stream(stream)),
+           "tq_read_kv_pages")
+    return outs[0], outs[1]

@@ -1,0 +1,158 @@
+// C ABI entry points of the page caches: argument validation and dispatch to the kernel
+// launchers. Checks that need no context come first, so that they hold (and can be tested)
+// without a device. No exception crosses this boundary.
+#include <cmath>
+#include <cstdio>
+
+#include "tq_internal.h"
+
+namespace {
+
+tq_status fail(tq_status st, const char* fn, const char* msg) {
+  char buf[512];
+  std::snprintf(buf, sizeof(buf), "%s: %s", fn, msg);
+  tq::set_last_error(buf);
+  return st;
+}
+
+tq_status fail_cuda(cudaError_t e, const char* fn) {
+  char buf[512];
+  std::snprintf(buf, sizeof(buf), "%s: %s (%s)", fn, cudaGetErrorName(e), cudaGetErrorString(e));
+  tq::set_last_error(buf);
+  return TQ_ECUDA;
+}
+
+bool aligned(const void* p, uintptr_t to) { return reinterpret_cast<uintptr_t>(p) % to == 0; }
+
+// Limits that keep every index below 2^62: rows in a cache or a call, and single strides.
+constexpr int64_t kMaxRows = int64_t(1) << 40, kMaxStride = int64_t(1) << 48;
+
+// A cache's description, as far as it can be judged without the context's d.
+tq_status check_pages(const char* fn, const tq_kv_pages* p) {
+  if (!p) return fail(TQ_EINVAL, fn, "NULL page cache");
+  if (p->format != TQ_KV_BF16 && p->format != TQ_KV_F16 && p->format != TQ_KV_MXFP4)
+    return fail(TQ_EINVAL, fn, "unknown page format");
+  if (p->pages_per_head != 0 && p->pages_per_head != 1) return fail(TQ_EINVAL, fn, "pages_per_head must be 0 or 1");
+  if (p->hkv < 1 || p->hkv > 65535) return fail(TQ_EINVAL, fn, "hkv must be in [1, 65535]");
+  if (p->page_size < 1 || p->page_size > (1 << 20)) return fail(TQ_EINVAL, fn, "page_size must be in [1, 2^20]");
+  if (p->n_pages < 1 || p->n_pages > kMaxRows / p->page_size || p->n_pages > 0x7fffffff)
+    return fail(TQ_EINVAL, fn, "n_pages out of range");
+  if (!p->k || !p->v) return fail(TQ_EINVAL, fn, "NULL pages");
+  if (!aligned(p->k, 16) || !aligned(p->v, 16)) return fail(TQ_EINVAL, fn, "pages must be 16-byte aligned");
+  if (p->format == TQ_KV_MXFP4 && (!p->k_scales || !p->v_scales)) return fail(TQ_EINVAL, fn, "NULL scales");
+  return TQ_OK;
+}
+
+// One array's strides: heads, tokens and pages must not overlap, and keep the alignment.
+bool strides_ok(const tq_kv_pages* p, int64_t page, int64_t tok, int64_t head, int64_t rec, int64_t mult) {
+  if (p->pages_per_head) head = rec;
+  for (int64_t s : {page, tok, head})
+    if (s < 0 || s > kMaxStride || s % mult) return false;
+  if (p->hkv > 1 && head < rec) return false;
+  if (p->page_size > 1 && tok < rec) return false;
+  if (p->n_pages > 1 && page < rec) return false;
+  const __int128 end = (__int128)page * p->n_pages + (__int128)tok * p->page_size + (__int128)head * p->hkv;
+  return end < ((__int128)1 << 61);
+}
+
+// The rest of the description, against the context; fills the kernels' view of it.
+tq_status view_pages(const char* fn, const tq_ctx* c, const tq_kv_pages* p, tq::PageView& w) {
+  if (!c) return fail(TQ_EINVAL, fn, "NULL context");
+  const int64_t d = c->shape.d;
+  const bool mx = p->format == TQ_KV_MXFP4;
+  const int64_t rec = mx ? d / 2 : d;
+  if (!strides_ok(p, p->page_stride, p->token_stride, p->head_stride, rec, mx ? 16 : 8))
+    return fail(TQ_EINVAL, fn, "page strides overlap a record, are unaligned or too large");
+  if (mx) {
+    if (!aligned(p->k_scales, d / 32) || !aligned(p->v_scales, d / 32))
+      return fail(TQ_EINVAL, fn, "scales must be aligned to d / 32 bytes");
+    if (!strides_ok(p, p->scale_page_stride, p->scale_token_stride, p->scale_head_stride, d / 32, d / 32))
+      return fail(TQ_EINVAL, fn, "scale strides overlap a record, are unaligned or too large");
+  }
+  int dev = -1;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev != c->device) {
+    cudaGetLastError();
+    return fail(TQ_EINVAL, fn, "the context belongs to another device than the current one");
+  }
+  const int64_t es = mx ? 1 : 2;
+  w.k = static_cast<char*>(p->k), w.v = static_cast<char*>(p->v);
+  w.ks = p->k_scales, w.vs = p->v_scales;
+  w.page_b = p->page_stride * es, w.tok_b = p->token_stride * es;
+  w.head_b = p->pages_per_head ? 0 : p->head_stride * es;
+  w.spage_b = mx ? p->scale_page_stride : 0, w.stok_b = mx ? p->scale_token_stride : 0;
+  w.shead_b = mx && !p->pages_per_head ? p->scale_head_stride : 0;
+  w.page_size = p->page_size, w.n_pages = p->n_pages, w.n_slots = p->n_pages * p->page_size;
+  w.hkv = p->hkv, w.per_head = p->pages_per_head;
+  return TQ_OK;
+}
+
+// The 16-bit type that goes with a page format (MXFP4: bf16, which holds its values).
+tq_dtype page_dtype(const tq_kv_pages* p) { return p->format == TQ_KV_F16 ? TQ_F16 : TQ_BF16; }
+
+// Rows of `width` elements, `stride` apart, `align`ed.
+bool rows_ok(const void* p, int64_t stride, int64_t width, int64_t n) {
+  return aligned(p, 16) && stride % 8 == 0 && stride <= kMaxStride / 1024 && (n <= 1 ? stride >= 0 : stride >= width);
+}
+
+}  // namespace
+
+extern "C" {
+
+tq_status tq_append_kv_pages(const tq_ctx* c, const tq_kv_pages* pages, tq_dtype dtype, int64_t n, int hq,
+                             const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+                             int64_t v_stride, const tq_rope* rope, const int64_t* slot, void* q_out,
+                             int64_t q_out_stride, void* stream) {
+  const char* fn = "tq_append_kv_pages";
+  if (n < 0 || n > kMaxRows) return fail(TQ_EINVAL, fn, "n out of range");
+  if (n == 0) return TQ_OK;
+  tq_status st = check_pages(fn, pages);
+  if (st != TQ_OK) return st;
+  if (dtype != page_dtype(pages))
+    return fail(dtype == TQ_F32 || dtype == TQ_BF16 || dtype == TQ_F16 ? TQ_EUNSUPPORTED : TQ_EINVAL, fn,
+                "q, k and v must be of a 16-bit cache's type (MXFP4: bf16)");
+  if (!k || !v || !slot) return fail(TQ_EINVAL, fn, "NULL k, v or slot map");
+  if (!aligned(slot, 8)) return fail(TQ_EINVAL, fn, "the slot map must be 8-byte aligned");
+  if ((q == nullptr) != (q_out == nullptr)) return fail(TQ_EINVAL, fn, "give both q and q_out or neither");
+  if (q && (hq < 1 || hq > 65535)) return fail(TQ_EINVAL, fn, "hq must be in [1, 65535]");
+  if (rope) {
+    if (rope->rot_dim < 0 || rope->rot_dim % 16)
+      return fail(TQ_EUNSUPPORTED, fn, "rot_dim must be a multiple of 16");
+    if (rope->interleaved != 0 && rope->interleaved != 1) return fail(TQ_EINVAL, fn, "interleaved must be 0 or 1");
+    if (rope->rot_dim > 0) {
+      if (!rope->cos_sin || !rope->positions) return fail(TQ_EINVAL, fn, "NULL rotation table or positions");
+      if (!aligned(rope->cos_sin, 16) || !aligned(rope->positions, 8))
+        return fail(TQ_EINVAL, fn, "the rotation table must be 16-byte and the positions 8-byte aligned");
+      if (rope->n_positions < 1 || rope->n_positions > kMaxRows)
+        return fail(TQ_EINVAL, fn, "n_positions out of range");
+    }
+  }
+  tq::PageView w;
+  if ((st = view_pages(fn, c, pages, w)) != TQ_OK) return st;
+  const int64_t d = c->shape.d;
+  if (rope && rope->rot_dim > d) return fail(TQ_EUNSUPPORTED, fn, "rot_dim above d");
+  if (!rows_ok(k, k_stride, pages->hkv * d, n) || !rows_ok(v, v_stride, pages->hkv * d, n) ||
+      (q && (!rows_ok(q, q_stride, hq * d, n) || !rows_ok(q_out, q_out_stride, hq * d, n))))
+    return fail(TQ_EINVAL, fn, "rows must be 16-byte aligned, strides multiples of 8 and at least a row");
+  cudaError_t e = tq::launch_kv_append(c, w, (int)pages->format, (int)dtype, n, hq, q, q_stride, k, k_stride, v,
+                                       v_stride, rope, slot, q_out, q_out_stride, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? TQ_OK : fail_cuda(e, fn);
+}
+
+tq_status tq_read_kv_pages(const tq_ctx* c, const tq_kv_pages* pages, int64_t n, const int64_t* slot, void* k_out,
+                           void* v_out, void* stream) {
+  const char* fn = "tq_read_kv_pages";
+  if (n < 0 || n > kMaxRows) return fail(TQ_EINVAL, fn, "n out of range");
+  if (n == 0) return TQ_OK;
+  tq_status st = check_pages(fn, pages);
+  if (st != TQ_OK) return st;
+  if (!slot || !aligned(slot, 8)) return fail(TQ_EINVAL, fn, "the slot map must be given and 8-byte aligned");
+  if (!k_out && !v_out) return fail(TQ_EINVAL, fn, "both outputs NULL");
+  if (!aligned(k_out, 16) || !aligned(v_out, 16)) return fail(TQ_EINVAL, fn, "outputs must be 16-byte aligned");
+  tq::PageView w;
+  if ((st = view_pages(fn, c, pages, w)) != TQ_OK) return st;
+  cudaError_t e = tq::launch_kv_read(c, w, (int)pages->format, n, slot, k_out, v_out,
+                                     static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? TQ_OK : fail_cuda(e, fn);
+}
+
+}  // extern "C"

@@ -254,8 +254,9 @@ tq_status tq_check_device(const tq_ctx* c, void* stream) {
   if (e != cudaSuccess) return fail_cuda(e, "tq_check_device");
   if (flag & 1u) return fail(TQ_ECUDA, "tq_check_device: a bounded wait for a bulk copy timed out; results of that call are invalid");
   if (flag & 4u)
-    return fail(TQ_EINVAL, "tq_check_device: a slot or page index was outside the caller's arrays; those vectors "
-                           "were not written (compression) or read as page 0 (decode)");
+    return fail(TQ_EINVAL, "tq_check_device: a slot, page, position or row range was outside the caller's arrays; "
+                           "those vectors were not written (compression, append) or not read (read), pages "
+                           "read as page 0 (decode), sequences skipped (prefill)");
   return TQ_OK;
 }
 

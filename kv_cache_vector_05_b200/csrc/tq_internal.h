@@ -151,6 +151,31 @@ cudaError_t launch_decompress(const tq_ctx* ctx, const uint8_t* k_codes, const u
                               const uint16_t* v_params, int64_t n_vec, float* k_out, float* v_out,
                               cudaStream_t stream);
 
+// ---- page caches (kv_append.cu) ----
+
+// Bits of the device error word: a slot, page, position or row range out of bounds.
+constexpr unsigned kErrIndex = 4u;
+
+// A tq_kv_pages as the kernels see it: byte strides, byte pointers.
+struct PageView {
+  char* k;
+  char* v;
+  uint8_t* ks;
+  uint8_t* vs;
+  int64_t page_b, tok_b, head_b;     // record strides in bytes
+  int64_t spage_b, stok_b, shead_b;  // scale strides in bytes
+  int64_t page_size, n_pages, n_slots;
+  int hkv;
+  int per_head;
+};
+
+cudaError_t launch_kv_append(const tq_ctx* ctx, const PageView& pg, int format, int dtype, int64_t n, int hq,
+                             const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+                             int64_t v_stride, const tq_rope* rope, const int64_t* slot, void* q_out,
+                             int64_t q_out_stride, cudaStream_t stream);
+cudaError_t launch_kv_read(const tq_ctx* ctx, const PageView& pg, int format, int64_t n, const int64_t* slot,
+                           void* k_out, void* v_out, cudaStream_t stream);
+
 // Records the message tq_last_error() returns on this thread (tq_api.cpp).
 void set_last_error(const char* msg);
 

@@ -1,0 +1,78 @@
+"""Refusals of the page-cache calls that need no device: bad sizes, pointers and combinations
+return the documented status, with the reason in tq_last_error, before any launch."""
+import ctypes
+
+import pytest
+
+T = pytest.importorskip("kv_cache_vector_05_b200")
+from kv_cache_vector_05_b200 import _lib  # noqa: E402
+
+lib, EINVAL, EUNSUP, OK = _lib.lib, _lib.TQ_EINVAL, _lib.TQ_EUNSUPPORTED, _lib.TQ_OK
+P = ctypes.c_void_p(1 << 20)                  # 16-byte aligned, never dereferenced
+ODD = ctypes.c_void_p((1 << 20) + 2)
+
+
+def pages(**kw):
+    s = _lib.tq_kv_pages()
+    s.format, s.hkv, s.pages_per_head, s.page_size, s.n_pages = _lib.TQ_KV_BF16, 2, 0, 16, 4
+    s.k = s.v = 1 << 20
+    s.page_stride, s.token_stride, s.head_stride = 16 * 256, 256, 128
+    for name, value in kw.items():
+        setattr(s, name, value)
+    return ctypes.byref(s)
+
+
+def append(pg, dtype=_lib.TQ_BF16, n=3, hq=4, q=P, k=P, v=P, rope=None, slot=P, q_out=P):
+    return lib.tq_append_kv_pages(None, pg, dtype, n, hq, q, hq * 128, k, 256, v, 256, rope, slot, q_out, hq * 128, None)
+
+
+BAD_PAGES = [
+    (dict(format=7), "format"), (dict(pages_per_head=2), "pages_per_head"), (dict(hkv=0), "hkv"),
+    (dict(hkv=1 << 17), "hkv"), (dict(page_size=0), "page_size"), (dict(page_size=(1 << 20) + 1), "page_size"),
+    (dict(n_pages=0), "n_pages"), (dict(n_pages=1 << 60), "n_pages"), (dict(k=None), "NULL pages"),
+    (dict(v=(1 << 20) + 8), "aligned"), (dict(format=_lib.TQ_KV_MXFP4), "NULL scales"),
+]
+
+
+@pytest.mark.parametrize("kw,msg", BAD_PAGES)
+def test_bad_page_caches(kw, msg):
+    assert append(pages(**kw)) == EINVAL and msg in lib.tq_last_error().decode()
+    assert lib.tq_read_kv_pages(None, pages(**kw), 3, P, P, P, None) == EINVAL
+    assert msg in lib.tq_last_error().decode()
+
+
+def test_append_refusals():
+    def why(status, msg, **kw):
+        assert append(pages(), **kw) == status and msg in lib.tq_last_error().decode(), (kw, lib.tq_last_error())
+    why(EINVAL, "n out of range", n=-1)
+    assert append(None) == EINVAL
+    why(EUNSUP, "16-bit", dtype=_lib.TQ_F32)
+    why(EUNSUP, "16-bit", dtype=_lib.TQ_F16)                      # not the cache's type
+    why(EINVAL, "16-bit", dtype=9)
+    why(EINVAL, "NULL k", k=None)
+    why(EINVAL, "NULL k", slot=None)
+    why(EINVAL, "8-byte", slot=ODD)
+    why(EINVAL, "both q", q_out=None)
+    why(EINVAL, "hq", hq=0)
+    for kw, status, msg in ((dict(rot_dim=24), EUNSUP, "multiple of 16"), (dict(rot_dim=-16), EUNSUP, "multiple of 16"),
+                            (dict(interleaved=3), EINVAL, "interleaved"), (dict(cos_sin=None), EINVAL, "NULL rotation"),
+                            (dict(positions=None), EINVAL, "NULL rotation"), (dict(cos_sin=ODD.value), EINVAL, "aligned"),
+                            (dict(n_positions=0), EINVAL, "n_positions")):
+        r = _lib.tq_rope(P.value, P.value, 10, 32, 0)
+        for name, value in kw.items():
+            setattr(r, name, value)
+        why(status, msg, rope=ctypes.byref(r))
+    why(EINVAL, "NULL context")
+    assert append(None, n=0, k=None) == OK                        # nothing to do before any pointer is examined
+
+
+def test_read_refusals():
+    assert lib.tq_read_kv_pages(None, pages(), -1, P, P, P, None) == EINVAL
+    assert lib.tq_read_kv_pages(None, pages(), 3, None, P, P, None) == EINVAL
+    assert lib.tq_read_kv_pages(None, pages(), 3, ODD, P, P, None) == EINVAL
+    assert lib.tq_read_kv_pages(None, pages(), 3, P, None, None, None) == EINVAL
+    assert "both outputs" in lib.tq_last_error().decode()
+    assert lib.tq_read_kv_pages(None, pages(), 3, P, ODD, P, None) == EINVAL
+    assert lib.tq_read_kv_pages(None, pages(), 3, P, P, P, None) == EINVAL       # no context
+    assert "NULL context" in lib.tq_last_error().decode()
+    assert lib.tq_read_kv_pages(None, None, 0, None, None, None, None) == OK
