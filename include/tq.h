@@ -437,6 +437,33 @@ tq_status tq_append_kv_pages(const tq_ctx* ctx, const tq_kv_pages* pages, tq_dty
 tq_status tq_read_kv_pages(const tq_ctx* ctx, const tq_kv_pages* pages, int64_t n, const int64_t* slot,
                            void* k_out, void* v_out, void* stream);
 
+/* Bytes of device workspace tq_decode_kv_pages needs. 0 for invalid arguments. */
+size_t tq_decode_kv_pages_workspace_bytes(const tq_ctx* ctx, int batch, int hq, int hkv);
+
+/* Attention of one new token per sequence over a page cache.
+ *   q           device [batch][hq][d] of q_dtype (rows q_stride elements apart, a multiple
+ *               of 8): the 16-bit cache's type, or TQ_BF16 for an MXFP4 cache
+ *   hq          a multiple of the cache's hkv; query head h reads KV head h / (hq / hkv)
+ *   block_table device int32 [batch][max_pages] ([batch][hkv][max_pages] with
+ *               pages_per_head): the page of each block of page_size tokens; only entries
+ *               that hold attended tokens are read. An entry outside [0, n_pages) sets the
+ *               device error word and reads page 0.
+ *   seq_lens    device int32 [batch] (clamped to [0, max_len]), or NULL for max_len
+ *   max_len     at most max_pages * page_size, and below 2^31
+ *   window      0, or the number of newest tokens attended
+ *   softmax_scale  logit scale; 0 selects 1/sqrt(d)
+ *   out         device [batch][hq][d] of out_dtype: TQ_F32 or q_dtype
+ *   lse         NULL, or device fp32 [batch][hq]: log sum_t exp(logit_t) (natural log)
+ * A sequence of length 0 gets a zero row and lse = -inf. Slots past a sequence's length or
+ * before its window may hold anything, infinities and NaN included.
+ * The workspace holds partial results within the call; calls that may overlap on the GPU
+ * need one each. */
+tq_status tq_decode_kv_pages(const tq_ctx* ctx, const tq_kv_pages* pages, const void* q, tq_dtype q_dtype,
+                             int64_t q_stride, int batch, int hq, const int32_t* block_table, int64_t max_pages,
+                             const int32_t* seq_lens, int64_t max_len, int64_t window, float softmax_scale,
+                             void* out, tq_dtype out_dtype, float* lse, void* workspace, size_t workspace_bytes,
+                             void* stream);
+
 #ifdef __cplusplus
 }
 #endif

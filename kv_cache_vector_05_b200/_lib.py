@@ -28,7 +28,7 @@ EXPORTED = (
     "tq_decode_workspace_bytes", "tq_decode_attention", "tq_decode_attention_paged", "tq_decompress",
     "tq_set_profile_events", "tq_check_device", "tq_decode_attention_static", "tq_decode_static_scratch_capacity",
     "tq_decode_attention_partial", "tq_merge_attention", "tq_set_decode_kernel", "tq_decode_kernel_for",
-    "tq_append_kv_pages", "tq_read_kv_pages",
+    "tq_append_kv_pages", "tq_read_kv_pages", "tq_decode_kv_pages_workspace_bytes", "tq_decode_kv_pages",
 )
 
 
@@ -137,6 +137,11 @@ def _load() -> ctypes.CDLL:
     lib.tq_append_kv_pages.restype = c_int
     lib.tq_read_kv_pages.argtypes = [vp, pages, i64, vp, vp, vp, vp]
     lib.tq_read_kv_pages.restype = c_int
+    lib.tq_decode_kv_pages_workspace_bytes.argtypes = [vp, c_int, c_int, c_int]
+    lib.tq_decode_kv_pages_workspace_bytes.restype = sz
+    lib.tq_decode_kv_pages.argtypes = [vp, pages, vp, c_int, i64, c_int, c_int, vp, i64, vp, i64, i64,
+                                       ctypes.c_float, vp, c_int, vp, vp, sz, vp]
+    lib.tq_decode_kv_pages.restype = c_int
     return lib
 
 
@@ -607,3 +612,59 @@ def tq_read_kv_pages(ctx: Context, pages: KVPages, slot, hkv: int, keys: bool = 
     _check(lib.tq_read_kv_pages(ctx.handle, p, n, _ptr(slot), _ptr(outs[0]), _ptr(outs[1]), _stream(stream)),
            "tq_read_kv_pages")
     return outs[0], outs[1]
+
+
+def _dtype_code(dtype) -> int:
+    import torch
+    return {torch.float32: TQ_F32, torch.bfloat16: TQ_BF16, torch.float16: TQ_F16}[dtype]
+
+
+def _table(block_table, batch: int, hkv: int, pages: KVPages):
+    import torch
+    lead = (batch, hkv) if pages.per_head else (batch,)
+    _index(block_table, "block_table", torch.int32, lead + (block_table.shape[-1],), pages)
+
+
+def _workspace(workspace, need: int, device):
+    import torch
+    if workspace is None:
+        return torch.empty(max(need, 256), dtype=torch.uint8, device=device)
+    if workspace.device != device or not workspace.is_contiguous():
+        raise ValueError(f"the workspace must be a contiguous tensor on {device}")
+    return workspace
+
+
+def tq_decode_kv_pages_workspace_bytes(ctx: Context, batch: int, hq: int, hkv: int) -> int:
+    return int(lib.tq_decode_kv_pages_workspace_bytes(ctx.handle, batch, hq, hkv))
+
+
+def tq_decode_kv_pages(ctx: Context, q, pages: KVPages, hkv: int, block_table, max_len: int, seq_lens=None,
+                       window: int = 0, softmax_scale: float = 0.0, out=None, out_dtype=None, lse=None,
+                       workspace=None, stream=None):
+    """Attention of one new token per sequence, q [batch, hq, d] (rows may be strided), over the
+    newest `window` (0: all) of its seq_lens (int32 [batch], or max_len) tokens in the page cache.
+    block_table: int32 [batch, max_pages], or [batch, hkv, max_pages] with per-head pages. `out`
+    [batch, hq, d] is fp32 or of q's type (`out_dtype`, default fp32, if it is allocated here).
+    Returns (out, lse [batch, hq] fp32), to be merged with other token ranges by tq_merge_attention."""
+    import torch
+    batch, hq = q.shape[0], q.shape[1]
+    p = pages.struct(ctx, hkv)
+    qs = _rows(q, "q", batch, ctx.d, pages)
+    _table(block_table, batch, hkv, pages)
+    if seq_lens is not None:
+        _index(seq_lens, "seq_lens", torch.int32, (batch,), pages)
+    if out is None:
+        out = torch.empty((batch, hq, ctx.d), dtype=out_dtype or torch.float32, device=q.device)
+    else:
+        _index(out, "out", out.dtype, (batch, hq, ctx.d), pages)
+    if lse is None:
+        lse = torch.empty((batch, hq), dtype=torch.float32, device=q.device)
+    else:
+        _index(lse, "lse", torch.float32, (batch, hq), pages)
+    need = lib.tq_decode_kv_pages_workspace_bytes(ctx.handle, batch, hq, hkv) if workspace is None else 0
+    workspace = _workspace(workspace, need, q.device)
+    _check(lib.tq_decode_kv_pages(
+        ctx.handle, p, _ptr(q), _dtype_code(q.dtype), qs, batch, hq, _ptr(block_table), block_table.shape[-1],
+        _ptr(seq_lens), max_len, window, softmax_scale, _ptr(out), _dtype_code(out.dtype), _ptr(lse),
+        _ptr(workspace), workspace.numel() * workspace.element_size(), _stream(stream)), "tq_decode_kv_pages")
+    return out, lse

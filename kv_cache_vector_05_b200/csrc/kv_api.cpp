@@ -94,6 +94,37 @@ bool rows_ok(const void* p, int64_t stride, int64_t width, int64_t n) {
   return aligned(p, 16) && stride % 8 == 0 && stride <= kMaxStride / 1024 && (n <= 1 ? stride >= 0 : stride >= width);
 }
 
+// Arguments the attention calls share, as far as they need no context.
+tq_status check_attention(const char* fn, const tq_kv_pages* p, const void* q, tq_dtype q_dtype, int batch, int hq,
+                          const int32_t* block_table, int64_t max_pages, const int32_t* seq_lens, int64_t max_len,
+                          int64_t window, float softmax_scale, const void* out, const float* lse,
+                          const void* workspace) {
+  tq_status st = check_pages(fn, p);
+  if (st != TQ_OK) return st;
+  if (q_dtype != page_dtype(p))
+    return fail(q_dtype == TQ_F32 || q_dtype == TQ_BF16 || q_dtype == TQ_F16 ? TQ_EUNSUPPORTED : TQ_EINVAL, fn,
+                "q must be of a 16-bit cache's type (MXFP4: bf16)");
+  if (hq < 1 || hq > 65535 || hq % p->hkv) return fail(TQ_EINVAL, fn, "hq must be a multiple of hkv in [1, 65535]");
+  if (!q || !out) return fail(TQ_EINVAL, fn, "NULL q or out");
+  if (!aligned(out, 16)) return fail(TQ_EINVAL, fn, "out must be 16-byte aligned");
+  if (!block_table) return fail(TQ_EINVAL, fn, "NULL block table");
+  if (!aligned(block_table, 4) || !aligned(seq_lens, 4) || !aligned(lse, 4))
+    return fail(TQ_EINVAL, fn, "block_table, seq_lens and lse must be 4-byte aligned");
+  if (max_len < 0 || max_len > 0x7fffff00) return fail(TQ_EINVAL, fn, "max_len out of range");
+  if (max_pages < 0 || max_pages > 0x7fffffff || max_pages * p->page_size < max_len)
+    return fail(TQ_EINVAL, fn, "max_pages below ceil(max_len / page_size)");
+  if (window < 0) return fail(TQ_EINVAL, fn, "negative window");
+  if (!std::isfinite(softmax_scale) || softmax_scale < 0.f)
+    return fail(TQ_EINVAL, fn, "softmax_scale must be finite and >= 0");
+  if ((double)batch * hq * (double)(max_len / 16 + 1) > 1e15) return fail(TQ_EINVAL, fn, "too many tokens");
+  if (!aligned(workspace, 16)) return fail(TQ_EINVAL, fn, "the workspace must be 16-byte aligned");
+  return TQ_OK;
+}
+
+float logit_scale(const tq_ctx* c, float softmax_scale) {
+  return softmax_scale > 0.f ? softmax_scale : 1.0f / std::sqrt((float)c->shape.d);
+}
+
 }  // namespace
 
 extern "C" {
@@ -152,6 +183,36 @@ tq_status tq_read_kv_pages(const tq_ctx* c, const tq_kv_pages* pages, int64_t n,
   if ((st = view_pages(fn, c, pages, w)) != TQ_OK) return st;
   cudaError_t e = tq::launch_kv_read(c, w, (int)pages->format, n, slot, k_out, v_out,
                                      static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? TQ_OK : fail_cuda(e, fn);
+}
+
+size_t tq_decode_kv_pages_workspace_bytes(const tq_ctx* c, int batch, int hq, int hkv) {
+  if (!c || batch < 0 || hq <= 0 || hkv <= 0 || hq % hkv) return 0;
+  return tq::kv_decode_workspace(c, hq / hkv);
+}
+
+tq_status tq_decode_kv_pages(const tq_ctx* c, const tq_kv_pages* pages, const void* q, tq_dtype q_dtype,
+                             int64_t q_stride, int batch, int hq, const int32_t* block_table, int64_t max_pages,
+                             const int32_t* seq_lens, int64_t max_len, int64_t window, float softmax_scale,
+                             void* out, tq_dtype out_dtype, float* lse, void* workspace, size_t workspace_bytes,
+                             void* stream) {
+  const char* fn = "tq_decode_kv_pages";
+  if (batch < 0) return fail(TQ_EINVAL, fn, "negative batch");
+  if (batch == 0) return TQ_OK;
+  tq_status st = check_attention(fn, pages, q, q_dtype, batch, hq, block_table, max_pages, seq_lens, max_len, window,
+                                 softmax_scale, out, lse, workspace);
+  if (st != TQ_OK) return st;
+  if (out_dtype != TQ_F32 && out_dtype != q_dtype)
+    return fail(TQ_EUNSUPPORTED, fn, "out must be fp32 or of q's type");
+  tq::PageView w;
+  if ((st = view_pages(fn, c, pages, w)) != TQ_OK) return st;
+  if (!rows_ok(q, q_stride, (int64_t)hq * c->shape.d, batch))
+    return fail(TQ_EINVAL, fn, "q rows must be 16-byte aligned, q_stride a multiple of 8 and at least a row");
+  if (!workspace || workspace_bytes < tq::kv_decode_workspace(c, hq / pages->hkv))
+    return fail(TQ_EINVAL, fn, "workspace missing or too small");
+  cudaError_t e = tq::launch_kv_decode(c, w, (int)pages->format, q, q_stride, batch, hq, block_table, max_pages,
+                                       seq_lens, max_len, window, logit_scale(c, softmax_scale), out,
+                                       out_dtype == TQ_F32, lse, workspace, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? TQ_OK : fail_cuda(e, fn);
 }
 

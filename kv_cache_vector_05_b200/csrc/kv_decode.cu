@@ -1,0 +1,937 @@
+// Attention of one new token per sequence over a page cache.
+//
+//   logit_t = scale <q, k_t>, p_t = 2^(log2e logit_t - m), out = sum_t p_t v_t / sum_t p_t
+//
+// over the tokens t of a sequence's window, for the G query heads that share a KV head. Each
+// cached record is read once and used by all G heads: 4 G d flop for 4 d bytes, so the kernel
+// is bound by HBM and everything else has to hide under the loads.
+//
+// Work. A unit is (sequence, KV head, block of at most 8 query heads); its tokens are cut into
+// tiles of 16. The tiles that hold tokens, of all units end to end, are split evenly over the
+// warps of the grid (lengths are read on the device, so a batch of varied lengths costs the
+// tokens it holds and no call synchronises). A warp is on its own until its range ends: it has
+// a private ring of stages in shared memory, filled by its own cp.async and guarded by
+// __syncwarp alone, and keeps the running maximum, sum and output of its heads in registers.
+// A unit that one warp finishes is written out directly. The pieces of a unit that several
+// warps of a CTA share are merged through shared memory, the pieces of several CTAs by
+// combine_kernel, both in a fixed order: results do not depend on timing.
+//
+// Tensor cores (mma.sync m16n8k16): S^T = K Q^T with the 16 tokens as rows and the heads as 8
+// columns, O^T = V^T P^T with 16 value coordinates as rows. A product's inner index may be
+// permuted freely, so a lane feeds K fragments with whole 16-byte chunks of a record (lane
+// (r, c) = (lane / 4, lane % 4) takes chunk c + 4 s of tokens r and r + 8), and the query's
+// fragments are the same chunks of q. V fragments pair two tokens per register: a lane takes
+// 16-byte chunks of tokens 2c, 2c + 1, 2c + 8, 2c + 9 and interleaves them with byte permutes.
+// P goes from the score layout (head pairs) to the operand layout (token pairs) by movmatrix.
+//
+// P enters its product as two 16-bit terms, high and low (16 bits for bf16, 21 for f16): with
+// at most 4 heads the low terms ride in the 4 free columns at no cost, with 5 to 8 they take a
+// second product.
+//
+// MXFP4 records: key codes become f16 operands by the conversion instruction (exact), the block
+// scale multiplies the fp32 sums of its 32 coordinates; the query is scaled by a power of two
+// per head so that its bf16 values fit f16. Value codes become exact bf16 values code 2^e: the
+// f16 code's bits moved to bf16's places are code 2^-112, one multiplication by 2^(112 + e)
+// finishes it (blocks of e > 15 or NaN take two multiplications). A key block of scale 2^-127,
+// the smallest, counts as zero.
+#include <algorithm>
+
+#include "kv_pages.cuh"
+#include "tq_device.cuh"
+#include "tq_sm100.cuh"
+
+namespace tq {
+namespace {
+
+using sm100::smem_u32;
+
+constexpr int kTile = 16;          // tokens per tile (one MMA row block)
+constexpr int kMinTiles = 2;       // fewest tiles a warp is given before CTAs are left out
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kNegHuge = -1.7e38f;  // maximum of no logits: finite, so that -inf - m is -inf
+
+struct DecArgs {
+  PageView pg;
+  const char* q;
+  int64_t q_b;
+  int batch, hq, G, HB, GB;        // GB query heads per block, HB blocks per KV head
+  const int32_t* table;
+  int64_t max_pages;
+  const int32_t* lens;
+  int64_t max_len, window;
+  float scale_log2;
+  char* out;
+  int out_f32;
+  float* lse;
+  float* head;   // [warps][GB][HD + 4]: pieces a warp leaves at its first unit's end
+  float* part;   // [2 CTAs][GB][HD + 4]: slot 2k CTA k's piece from its range's start, 2k + 1 a later one
+  int4* meta;    // [CTAs]: {sequence, unit of it, last CTA, 1} of a unit begun in this CTA and shared
+  unsigned int* err;
+};
+
+// Format, head dimension -> warps per CTA and ring stages (one CTA per SM).
+template <int FMT, int HD>
+struct Config {
+  static constexpr bool MX = FMT == TQ_KV_MXFP4;
+  static constexpr int kWarps = MX ? (HD == 256 ? 8 : 16) : (HD == 256 ? 4 : 8);
+  static constexpr int kPitch = MX ? HD / 2 + 16 : HD * 2;       // bytes between records of a stage
+  static constexpr int kBlocks = HD / 32;                        // scale bytes of an MXFP4 record
+  static constexpr int kScale = MX ? (kBlocks < 4 ? 4 : kBlocks) : 0;  // their room in a stage
+  static constexpr int kStageBytes = 2 * kTile * (kPitch + kScale);
+  static constexpr int kStages = MX ? 5 : (HD == 64 ? 6 : 3);
+  static constexpr int kRing = kStages * kStageBytes;
+  static constexpr int kSmem = kWarps * kRing;
+};
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+template <typename T>
+__device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                         uint32_t b0, uint32_t b1) {
+  if constexpr (sizeof(T) == 2 && std::is_same<T, __half>::value)
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+  else
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+  uint32_t y;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+
+// Copies of `bytes` (4, 8 or 16); zero fill where !valid.
+template <int BYTES>
+__device__ __forceinline__ void cp_async(uint32_t dst, const void* src, bool valid) {
+  const int n = valid ? BYTES : 0;
+  if constexpr (BYTES == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(BYTES), "r"(n) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ uint32_t lds32(uint32_t a) {
+  uint32_t v;
+  asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(a));
+  return v;
+}
+
+// 16-byte chunk permutation of token row `row` in a 16-bit stage: the chunks that the 8 lanes
+// of a shared-memory phase read (key fragments: 2 rows x 4 chunks; value fragments: 4 even or
+// 4 odd rows x 2 chunks) fall on distinct banks.
+__device__ __forceinline__ int chunk_swizzle(int row) { return (((row >> 1) & 3) << 1) ^ ((row & 1) << 2); }
+
+// First token and tiles of a sequence: its attended tokens are [lo, len).
+struct Extent {
+  int len, lo, nt;
+};
+__device__ __forceinline__ Extent extent(const DecArgs& a, int b) {
+  int64_t n = a.lens ? (int64_t)__ldg(a.lens + b) : a.max_len;
+  n = n < 0 ? 0 : n > a.max_len ? a.max_len : n;
+  Extent e;
+  e.len = (int)n;
+  e.lo = a.window && n > a.window ? (int)(n - a.window) : 0;
+  e.nt = e.len ? (e.len - 1) / kTile - e.lo / kTile + 1 : 0;
+  return e;
+}
+
+// A position in the work: tile `tile` of unit `uk` of sequence `b`, and the page of its block.
+struct Cursor {
+  Extent e;
+  int b, uk, tile;
+  int blk;      // block-table index of the tile's first token
+  int off;      // its place in the page (pages of whole tiles)
+  int64_t page; // page id, loaded ahead of its use
+};
+
+template <typename T, int FMT, int HD, bool SMALL, bool WHOLE>
+struct Worker {
+  using C = Config<FMT, HD>;
+  static constexpr bool MX = C::MX;
+  static constexpr int NK = HD / 32;       // 32-coordinate steps of the score product
+  static constexpr int NM = HD / 16;       // 16-coordinate row blocks of the output product
+  // P's operand range: bf16 has fp32's exponents; for f16 the largest p is 2^13 to 2^15, so that
+  // the smallest step, 2^-24, is at most 2^-37 of it
+  static constexpr bool F16P = !MX && FMT == TQ_KV_F16;
+  static constexpr float kOff = F16P ? 13.f : 0.f;
+  static constexpr float kSlack = F16P ? 2.f : 8.f;
+  static constexpr float kLeast = F16P ? 5.9604644775390625e-8f : 1.17549435e-38f;
+
+  const DecArgs& a;
+  const int lane, r, c;
+  const uint32_t ring;
+  uint32_t q[NK][4];
+  float sl[2];
+  float acc[NM][4];
+  float m[2], l[2];
+
+  __device__ Worker(const DecArgs& args, uint32_t ring_base, int ln)
+      : a(args), lane(ln), r(ln >> 2), c(ln & 3), ring(ring_base) {}
+
+  // ---- loads ------------------------------------------------------------------------
+
+  __device__ __forceinline__ int64_t page_of(const Cursor& u, int blk) const {
+    const int64_t row = a.pg.per_head ? (int64_t)u.b * a.pg.hkv + u.uk / a.HB : u.b;
+    int64_t p = __ldg(a.table + row * a.max_pages + blk);
+    if (p < 0 || p >= a.pg.n_pages) {
+      atomicOr(a.err, kErrIndex);
+      p = 0;
+    }
+    return p;
+  }
+
+  // Enter unit (b, uk) at `tile`; the page of the tile is looked up at once for WHOLE pages.
+  __device__ __forceinline__ void place(Cursor& u) const {
+    if constexpr (WHOLE) {
+      const int t = (u.e.lo / kTile + u.tile) * kTile;
+      u.blk = t / (int)a.pg.page_size;
+      u.off = t - u.blk * (int)a.pg.page_size;
+      u.page = page_of(u, u.blk);
+    }
+  }
+  __device__ __forceinline__ void advance(Cursor& u) const {
+    if (++u.tile < u.e.nt) {
+      if constexpr (WHOLE) {
+        u.off += kTile;
+        if (u.off == (int)a.pg.page_size) {
+          u.off = 0;
+          u.page = page_of(u, ++u.blk);
+        }
+      }
+      return;
+    }
+    u.tile = 0;
+    if (++u.uk == a.pg.hkv * a.HB) {
+      u.uk = 0;
+      do {
+        u.e = extent(a, ++u.b);
+      } while (u.e.nt == 0);
+    }
+    place(u);
+  }
+
+  // Start the copies of the cursor's tile into ring stage `st`. Tokens outside [lo, len) are
+  // filled with zeros: their probabilities are zero, and what the cache holds there must not
+  // reach a product.
+  __device__ __forceinline__ void issue(const Cursor& u, int st) const {
+    const uint32_t base = ring + st * C::kStageBytes;
+    const int t = (u.e.lo / kTile + u.tile) * kTile;
+    const int kvh = u.uk / a.HB;
+    int64_t off0 = 0, soff0 = 0;
+    if constexpr (WHOLE) {
+      off0 = u.page * a.pg.page_b + (int64_t)u.off * a.pg.tok_b + (int64_t)kvh * a.pg.head_b;
+      if constexpr (MX) soff0 = u.page * a.pg.spage_b + (int64_t)u.off * a.pg.stok_b + (int64_t)kvh * a.pg.shead_b;
+    } else {
+      // each of 16 lanes looks up one token's page; the others receive it by shuffles
+      int tok = t + (lane & 15);
+      tok = tok < u.e.lo ? u.e.lo : tok >= u.e.len ? u.e.len - 1 : tok;
+      const int blk = tok / (int)a.pg.page_size, o = tok - blk * (int)a.pg.page_size;
+      const int64_t pg = page_of(u, blk);
+      off0 = pg * a.pg.page_b + (int64_t)o * a.pg.tok_b + (int64_t)kvh * a.pg.head_b;
+      if constexpr (MX) soff0 = pg * a.pg.spage_b + (int64_t)o * a.pg.stok_b + (int64_t)kvh * a.pg.shead_b;
+    }
+    constexpr int CPR = MX ? HD / 32 : HD / 8;  // 16-byte chunks per record
+    constexpr int RP = 32 / CPR;                // records per instruction
+    const int row0 = lane / CPR, ch = lane % CPR;
+#pragma unroll
+    for (int j = 0; j < (kTile + RP - 1) / RP; ++j) {
+      const int row = row0 + j * RP;
+      if (RP > kTile && row >= kTile) break;
+      const bool ok = t + row >= u.e.lo && t + row < u.e.len;
+      const int64_t off = (WHOLE ? off0 + (int64_t)row * a.pg.tok_b : __shfl_sync(kFull, off0, row)) + ch * 16;
+      const uint32_t dst = base + row * C::kPitch + (MX ? ch : (ch ^ chunk_swizzle(row))) * 16;
+      cp_async<16>(dst, a.pg.k + off, ok);
+      cp_async<16>(dst + kTile * C::kPitch, a.pg.v + off, ok);
+    }
+    if constexpr (MX) {
+      const int row = lane & 15;
+      const bool ok = t + row >= u.e.lo && t + row < u.e.len;
+      const int64_t off = WHOLE ? soff0 + (int64_t)row * a.pg.stok_b : soff0;
+      const uint8_t* src = (lane < 16 ? a.pg.ks : a.pg.vs) + off;
+      const uint32_t dst = base + 2 * kTile * C::kPitch + lane * C::kScale;
+      if constexpr (C::kBlocks == 2) {  // below cp.async's sizes
+        const uint32_t w = ok ? *reinterpret_cast<const uint16_t*>(src) : 0u;
+        asm volatile("st.shared.b32 [%0], %1;" ::"r"(dst), "r"(w) : "memory");
+      } else {
+        cp_async<C::kBlocks>(dst, src, ok);
+      }
+    }
+  }
+
+  // ---- one unit's queries -------------------------------------------------------------
+
+  __device__ __forceinline__ void begin(const Cursor& u) {
+    const int kvh = u.uk / a.HB, hb = u.uk - kvh * a.HB;
+    const int heads = min(a.GB, a.G - hb * a.GB);
+    const int col = lane >> 2, head = SMALL ? col & 3 : col;
+    const bool ok = head < heads;
+    const char* src = a.q + (int64_t)u.b * a.q_b + ((int64_t)kvh * a.G + hb * a.GB + head) * (HD * 2);
+#pragma unroll
+    for (int s = 0; s < NK; ++s) {
+      const uint4 x = ok ? __ldg(reinterpret_cast<const uint4*>(src) + c + 4 * s) : make_uint4(0, 0, 0, 0);
+      q[s][0] = x.x, q[s][1] = x.y, q[s][2] = x.z, q[s][3] = x.w;
+    }
+    sl[0] = sl[1] = a.scale_log2;
+    if constexpr (MX) {
+      // f16 operands: scale the head by 2^sh so that its largest magnitude is in [2^13, 2^14)
+      uint32_t mx = 0;
+#pragma unroll
+      for (int s = 0; s < NK; ++s)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) mx = max(mx, max((q[s][i] << 16) & 0x7fffffffu, q[s][i] & 0x7fff0000u));
+      mx = max(mx, __shfl_xor_sync(kFull, mx, 1));
+      mx = max(mx, __shfl_xor_sync(kFull, mx, 2));
+      int sh = 13 + 127 - (int)(mx >> 23);
+      sh = mx >= 0x7f800000u || mx == 0 ? 0 : max(-100, min(100, sh));
+      const float f = __uint_as_float((uint32_t)(127 + sh) << 23);
+#pragma unroll
+      for (int s = 0; s < NK; ++s)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float2 x = Half2<__nv_bfloat16>::unpack(q[s][i]);
+          q[s][i] = Half2<__half>::pack(x.x * f, x.y * f);
+        }
+      const float back = __uint_as_float((uint32_t)(127 - sh) << 23);
+      sl[0] *= __shfl_sync(kFull, back, (2 * c) * 4);
+      sl[1] *= __shfl_sync(kFull, back, (2 * c + 1) * 4);
+    }
+#pragma unroll
+    for (int i = 0; i < NM; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
+    m[0] = m[1] = kNegHuge;
+    l[0] = l[1] = 0.f;
+  }
+
+  // ---- one tile -----------------------------------------------------------------------
+
+  // SLOW: some scale byte of the tile needs the full range (see the top comment).
+  template <bool SLOW>
+  __device__ __forceinline__ void scores(uint32_t base, float (&s)[4]) const {
+    if constexpr (!MX) {
+      float s2[4] = {0.f, 0.f, 0.f, 0.f};
+      const uint32_t row = base + r * C::kPitch;
+      const int sw = chunk_swizzle(r);
+#pragma unroll
+      for (int i = 0; i < NK; ++i) {
+        const uint32_t at = row + ((c + 4 * i) ^ sw) * 16;
+        const uint4 x = lds128(at), y = lds128(at + 8 * C::kPitch);
+        mma16816<T>(s, x.x, y.x, x.y, y.y, q[i][0], q[i][1]);
+        mma16816<T>(s2, x.z, y.z, x.w, y.w, q[i][2], q[i][3]);
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) s[i] += s2[i];
+    } else {
+      const uint32_t row = base + r * C::kPitch + c * 4;
+      const uint32_t srow = base + 2 * kTile * C::kPitch + r * C::kScale;
+#pragma unroll
+      for (int i = 0; i < NK; ++i) {
+        uint32_t x[4], y[4];
+        e2m1x8_f16(lds32(row + i * 16), x);
+        e2m1x8_f16(lds32(row + 8 * C::kPitch + i * 16), y);
+        float g[4] = {0.f, 0.f, 0.f, 0.f};
+        mma16816<__half>(g, x[0], y[0], x[1], y[1], q[i][0], q[i][1]);
+        mma16816<__half>(g, x[2], y[2], x[3], y[3], q[i][2], q[i][3]);
+        const uint32_t w0 = lds32(srow + (i & ~3)), w1 = lds32(srow + 8 * C::kScale + (i & ~3));
+        const uint32_t b0 = (w0 >> (8 * (i & 3))) & 255u, b1 = (w1 >> (8 * (i & 3))) & 255u;
+        const float f0 = SLOW ? e8m0(b0) : __uint_as_float(b0 << 23), f1 = SLOW ? e8m0(b1) : __uint_as_float(b1 << 23);
+        s[0] = fmaf(g[0], f0, s[0]);
+        s[1] = fmaf(g[1], f0, s[1]);
+        s[2] = fmaf(g[2], f1, s[2]);
+        s[3] = fmaf(g[3], f1, s[3]);
+      }
+    }
+  }
+
+  // Token pair (a, b) of 8 coordinates: out[e] = (a's, b's) coordinate e.
+  static __device__ __forceinline__ void interleave(const uint4& x, const uint4& y, uint32_t (&out)[8]) {
+    const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      out[2 * i] = __byte_perm(xs[i], ys[i], 0x5410);
+      out[2 * i + 1] = __byte_perm(xs[i], ys[i], 0x7632);
+    }
+  }
+  // The same for MXFP4 words with scale factors `f` (bf16 pair): exact bf16 values.
+  template <bool SLOW>
+  static __device__ __forceinline__ void interleave4(uint32_t x, uint32_t y, uint32_t f, uint32_t (&out)[8]) {
+    const uint32_t even = (x & 0x0f0f0f0fu) | ((y << 4) & 0xf0f0f0f0u);
+    const uint32_t odd = ((x >> 4) & 0x0f0f0f0fu) | (y & 0xf0f0f0f0u);
+    uint32_t he[4], ho[4];
+    e2m1x8_f16(even, he);
+    e2m1x8_f16(odd, ho);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const uint32_t h = i & 1 ? ho[i >> 1] : he[i >> 1];
+      const uint32_t w = (h & 0x80008000u) | ((h >> 3) & 0x0fff0fffu);  // code 2^-112 as bf16
+      __nv_bfloat162 t = *reinterpret_cast<const __nv_bfloat162*>(&w);
+      if constexpr (SLOW) {
+        const uint32_t k = 0x77807780u;  // 2^112
+        t = __hmul2(t, *reinterpret_cast<const __nv_bfloat162*>(&k));
+      }
+      t = __hmul2(t, *reinterpret_cast<const __nv_bfloat162*>(&f));
+      out[i] = *reinterpret_cast<const uint32_t*>(&t);
+    }
+  }
+
+  template <bool SLOW>
+  __device__ __forceinline__ void values(uint32_t base, uint32_t bh0, uint32_t bh1, uint32_t bl0, uint32_t bl1) {
+    const uint32_t v = base + kTile * C::kPitch;
+    constexpr int NC = HD / 64;  // 8-coordinate chunks per lane and token
+    using TV = typename std::conditional<MX, __nv_bfloat16, T>::type;
+    uint32_t sc[4][2];
+    if constexpr (MX) {
+      const uint32_t sv = base + (2 * C::kPitch + C::kScale) * kTile;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int tok = 2 * c + (i & 1) + (i >> 1) * 8;
+        sc[i][0] = lds32(sv + tok * C::kScale);
+        sc[i][1] = C::kBlocks == 8 ? lds32(sv + tok * C::kScale + 4) : 0u;
+      }
+    }
+    // chunk n of the tile's tokens: pairs (2c, 2c + 1) in lo, (2c + 8, 2c + 9) in hi
+    auto load = [&](int n, uint32_t (&lo)[8], uint32_t (&hi)[8]) {
+      if constexpr (!MX) {
+        const int ch = r + 8 * n;
+        uint4 x[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int tok = 2 * c + (i & 1) + (i >> 1) * 8;
+          x[i] = lds128(v + tok * C::kPitch + ((ch ^ chunk_swizzle(tok)) * 16));
+        }
+        interleave(x[0], x[1], lo);
+        interleave(x[2], x[3], hi);
+      } else {
+        uint32_t x[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int tok = 2 * c + (i & 1) + (i >> 1) * 8;
+          x[i] = lds32(v + tok * C::kPitch + (r + 8 * n) * 4);
+        }
+        // the chunk lies in block 2 n + r / 4
+        const uint32_t sel = (uint32_t)((2 * n & 3) + (r >> 2)) * 0x1111u + 0x4400u;
+        uint32_t f[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const uint32_t z = __byte_perm(sc[2 * i][n >> 1], sc[2 * i + 1][n >> 1], sel) & 0x00ff00ffu;
+          f[i] = SLOW ? e8m0_bf16(z & 255u) | (e8m0_bf16(z >> 16) << 16)  // 2^e
+                      : (z << 7) + 0x38003800u;                           // 2^(112 + e)
+        }
+        interleave4<SLOW>(x[0], x[1], f[0], lo);
+        interleave4<SLOW>(x[2], x[3], f[1], hi);
+      }
+    };
+    auto product = [&](float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
+      mma16816<TV>(d, a0, a1, a2, a3, bh0, bh1);
+      if constexpr (!SMALL) mma16816<TV>(d, a0, a1, a2, a3, bl0, bl1);
+    };
+    if constexpr (NC == 1) {
+      uint32_t lo[8], hi[8];
+      load(0, lo, hi);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) product(acc[i], lo[2 * i], lo[2 * i + 1], hi[2 * i], hi[2 * i + 1]);
+    } else {
+#pragma unroll
+      for (int n = 0; n < NC; n += 2) {
+        uint32_t lo0[8], hi0[8], lo1[8], hi1[8];
+        load(n, lo0, hi0);
+        load(n + 1, lo1, hi1);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) product(acc[n * 4 + i], lo0[i], lo1[i], hi0[i], hi1[i]);
+      }
+    }
+  }
+
+  template <bool SLOW>
+  __device__ __forceinline__ void tile(const Cursor& u, uint32_t base) {
+    using TP = typename std::conditional<F16P, __half, __nv_bfloat16>::type;
+    float s[4] = {0.f, 0.f, 0.f, 0.f};
+    scores<SLOW>(base, s);
+    s[0] *= sl[0], s[1] *= sl[1], s[2] *= sl[0], s[3] *= sl[1];
+    const int t = (u.e.lo / kTile + u.tile) * kTile;
+    if (t < u.e.lo || t + kTile > u.e.len) {
+      if (t + r < u.e.lo || t + r >= u.e.len) s[0] = s[1] = -INFINITY;
+      if (t + r + 8 < u.e.lo || t + r + 8 >= u.e.len) s[2] = s[3] = -INFINITY;
+    }
+    // m is moved only when a logit passes it by kSlack (then p would leave its range)
+    const float x0 = fmaxf(s[0], s[2]), x1 = fmaxf(s[1], s[3]);
+    if (__any_sync(kFull, x0 > m[0] + (kOff + kSlack) || x1 > m[1] + (kOff + kSlack))) {
+      float n[2] = {x0, x1};
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+#pragma unroll
+        for (int o = 4; o < 32; o <<= 1) n[j] = fmaxf(n[j], __shfl_xor_sync(kFull, n[j], o));
+        n[j] = fmaxf(n[j] - kOff, m[j]);
+        const float f = ex2(m[j] - n[j]);
+        m[j] = n[j];
+        l[j] *= f;
+#pragma unroll
+        for (int i = 0; i < NM; ++i) acc[i][j] *= f, acc[i][2 + j] *= f;
+      }
+    }
+    float p[4];
+    p[0] = ex2(s[0] - m[0]), p[1] = ex2(s[1] - m[1]), p[2] = ex2(s[2] - m[0]), p[3] = ex2(s[3] - m[1]);
+    l[0] += p[0] + p[2];
+    l[1] += p[1] + p[3];
+    // The high term is rounded towards zero and the low one kept above it, so that an infinite
+    // value meets two positive factors and stays infinite.
+    uint32_t h0 = Half2<TP>::pack_rz(p[0], p[1]), h1 = Half2<TP>::pack_rz(p[2], p[3]);
+    const float2 g0 = Half2<TP>::unpack(h0), g1 = Half2<TP>::unpack(h1);
+    const uint32_t l0 = Half2<TP>::pack(fmaxf(p[0] - g0.x, kLeast), fmaxf(p[1] - g0.y, kLeast));
+    const uint32_t l1 = Half2<TP>::pack(fmaxf(p[2] - g1.x, kLeast), fmaxf(p[3] - g1.y, kLeast));
+    if constexpr (SMALL) {  // columns 4 to 7 hold the same heads' low terms
+      h0 = c < 2 ? h0 : l0;
+      h1 = c < 2 ? h1 : l1;
+      values<SLOW>(base, transpose8x8(h0), transpose8x8(h1), 0, 0);
+    } else {
+      values<SLOW>(base, transpose8x8(h0), transpose8x8(h1), transpose8x8(l0), transpose8x8(l1));
+    }
+  }
+
+  __device__ __forceinline__ void step(const Cursor& u, int st) {
+    const uint32_t base = ring + st * C::kStageBytes;
+    if constexpr (MX) {
+      // lane i's scale word of the tile: 16 key rows, then 16 value rows
+      uint32_t w = lds32(base + 2 * kTile * C::kPitch + lane * C::kScale);
+      uint32_t w2 = C::kBlocks == 8 ? lds32(base + 2 * kTile * C::kPitch + lane * C::kScale + 4) : 0u;
+      w = __vmaxu4(w, w2);
+      const uint32_t limit = lane < 16 ? 0xfefefefeu : 0x8e8e8e8eu;  // keys: not NaN; values: e <= 15
+      if (__any_sync(kFull, __vmaxu4(w, limit) != limit)) {
+        tile<true>(u, base);
+        return;
+      }
+    }
+    tile<false>(u, base);
+  }
+
+  // ---- results ------------------------------------------------------------------------
+
+  // Sum the lanes' shares: l over the tokens, and the low terms' columns.
+  __device__ __forceinline__ void finish() {
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+      for (int o = 4; o < 32; o <<= 1) l[j] += __shfl_xor_sync(kFull, l[j], o);
+    if constexpr (SMALL) {
+#pragma unroll
+      for (int i = 0; i < NM; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[i][j] += __shfl_xor_sync(kFull, acc[i][j], 2);
+    }
+  }
+
+  // f(head, first coordinate, 8 values) for this lane's heads and chunks.
+  template <typename F>
+  __device__ __forceinline__ void each(int heads, F&& f) const {
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const int h = 2 * c + j;
+      if (h >= heads || (SMALL && c >= 2)) continue;
+      if constexpr (HD == 64) {
+        const float x[8] = {acc[0][j], acc[0][2 + j], acc[1][j], acc[1][2 + j],
+                            acc[2][j], acc[2][2 + j], acc[3][j], acc[3][2 + j]};
+        f(h, j, 8 * r, x);
+      } else {
+#pragma unroll
+        for (int n = 0; n < HD / 64; ++n) {
+          const int i = (n >> 1) * 8, k = (n & 1) * 2 + j;
+          const float x[8] = {acc[i][k],     acc[i + 1][k], acc[i + 2][k], acc[i + 3][k],
+                              acc[i + 4][k], acc[i + 5][k], acc[i + 6][k], acc[i + 7][k]};
+          f(h, j, 8 * (r + 8 * n), x);
+        }
+      }
+    }
+  }
+
+  __device__ __forceinline__ void write_out(const Cursor& u) const {
+    const int kvh = u.uk / a.HB, hb = u.uk - kvh * a.HB;
+    const int heads = min(a.GB, a.G - hb * a.GB);
+    const int64_t row0 = (int64_t)u.b * a.hq + kvh * a.G + hb * a.GB;
+    each(heads, [&](int h, int j, int d0, const float (&x)[8]) {
+      const float inv = l[j] == 0.f ? 0.f : 1.f / l[j];  // no finite logit at all: zeros
+      if (a.lse && d0 == 0) a.lse[row0 + h] = (m[j] + log2f(l[j])) * kLn2;
+      const int64_t at = (row0 + h) * HD + d0;
+      if (a.out_f32) {
+        float4* o = reinterpret_cast<float4*>(a.out) + at / 4;
+        o[0] = make_float4(x[0] * inv, x[1] * inv, x[2] * inv, x[3] * inv);
+        o[1] = make_float4(x[4] * inv, x[5] * inv, x[6] * inv, x[7] * inv);
+      } else {
+        *(reinterpret_cast<uint4*>(a.out) + at / 8) =
+            make_uint4(Half2<T>::pack(x[0] * inv, x[1] * inv), Half2<T>::pack(x[2] * inv, x[3] * inv),
+                       Half2<T>::pack(x[4] * inv, x[5] * inv), Half2<T>::pack(x[6] * inv, x[7] * inv));
+      }
+    });
+  }
+
+  // [GB][HD + 4]: output sums, then m and l
+  __device__ __forceinline__ void write_piece(float* dst, int heads) const {
+    each(heads, [&](int h, int j, int d0, const float (&x)[8]) {
+      float4* o = reinterpret_cast<float4*>(dst + h * (HD + 4) + d0);
+      o[0] = make_float4(x[0], x[1], x[2], x[3]);
+      o[1] = make_float4(x[4], x[5], x[6], x[7]);
+      if (d0 == 0) *reinterpret_cast<float2*>(dst + h * (HD + 4) + HD) = make_float2(m[j], l[j]);
+    });
+  }
+};
+
+// Output row element of merged sums: out[row][d0..d0+3].
+__device__ __forceinline__ void store4(const DecArgs& a, bool f16, int64_t at, float4 x) {
+  if (a.out_f32) {
+    *reinterpret_cast<float4*>(reinterpret_cast<float*>(a.out) + at) = x;
+  } else {
+    const uint2 w = f16 ? make_uint2(Half2<__half>::pack(x.x, x.y), Half2<__half>::pack(x.z, x.w))
+                        : make_uint2(Half2<__nv_bfloat16>::pack(x.x, x.y), Half2<__nv_bfloat16>::pack(x.z, x.w));
+    *reinterpret_cast<uint2*>(a.out + at * 2) = w;
+  }
+}
+
+__device__ __forceinline__ int64_t warp_incl_scan(int64_t v, int lane) {
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t y = __shfl_up_sync(kFull, v, o);
+    if (lane >= o) v += y;
+  }
+  return v;
+}
+
+template <typename T, int FMT, int HD, bool SMALL, bool WHOLE>
+__global__ void __launch_bounds__(Config<FMT, HD>::kWarps * 32, 1) kv_decode_kernel(const DecArgs a) {
+  using C = Config<FMT, HD>;
+  constexpr int W = C::kWarps, NT = W * 32, kRow = HD + 4;
+  extern __shared__ __align__(128) unsigned char smem[];
+  __shared__ int64_t s_scan[W];
+  __shared__ int64_t s_start;
+  __shared__ int s_b;
+  __shared__ int64_t s_tile0[2 * W];                       // pieces: first tile of the whole order
+  __shared__ int s_pb[2 * W], s_uk[2 * W], s_from[2 * W], s_to[2 * W], s_nt[2 * W];
+  const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
+  const int upb = a.pg.hkv * a.HB;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+
+  // sequences without tokens: zero rows
+  for (int b = blockIdx.x; b < a.batch; b += gridDim.x) {
+    if (extent(a, b).nt) continue;
+    for (int i = tid; i < a.hq * (HD / 4); i += NT)
+      store4(a, std::is_same<T, __half>::value, (int64_t)b * a.hq * HD + i * 4, make_float4(0.f, 0.f, 0.f, 0.f));
+    if (a.lse)
+      for (int h = tid; h < a.hq; h += NT) a.lse[(int64_t)b * a.hq + h] = -INFINITY;
+  }
+
+  // all tiles, then the sequence in which this CTA's range starts
+  int64_t sum = 0;
+  for (int b = tid; b < a.batch; b += NT) sum += extent(a, b).nt;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kFull, sum, o);
+  if (lane == 0) s_scan[w] = sum;
+  __syncthreads();
+  int64_t total = 0;
+#pragma unroll
+  for (int i = 0; i < W; ++i) total += s_scan[i];
+  total *= upb;
+  const int64_t want = (total + W * kMinTiles - 1) / (W * kMinTiles);
+  const int n = (int)(want < gridDim.x ? want : gridDim.x);
+  const int k = blockIdx.x;
+  if (tid == 0) a.meta[k] = make_int4(0, 0, 0, 0);
+  if (k >= n) return;
+  const int64_t cta0 = total * k / n;
+  for (int64_t base = 0, b0 = 0;; b0 += NT) {
+    const int b = (int)b0 + tid;
+    const int64_t mine = b < a.batch ? (int64_t)extent(a, b).nt * upb : 0;
+    const int64_t incl = warp_incl_scan(mine, lane);
+    __syncthreads();  // s_scan has been read
+    if (lane == 31) s_scan[w] = incl;
+    __syncthreads();
+    int64_t before = base, all = base;
+#pragma unroll
+    for (int i = 0; i < W; ++i) {
+      if (i < w) before += s_scan[i];
+      all += s_scan[i];
+    }
+    if (mine && before + incl - mine <= cta0 && cta0 < before + incl) {
+      s_b = b;
+      s_start = before + incl - mine;
+    }
+    base = all;
+    if (cta0 < base) break;
+  }
+  __syncthreads();
+
+  const int64_t nw = (int64_t)n * W, gw = (int64_t)k * W + w;
+  const int64_t r0 = total * gw / nw, r1 = total * (gw + 1) / nw;
+  if (lane < 2) s_pb[2 * w + lane] = -1;
+  Worker<T, FMT, HD, SMALL, WHOLE> wk(a, smem_u32(smem) + w * C::kRing, lane);
+  Cursor ld{}, cur{};
+  int seg_from = 0;
+  bool open = false;
+  if (r0 < r1) {
+    int64_t start = s_start;
+    cur.b = s_b;
+    cur.e = extent(a, cur.b);
+    while (r0 >= start + (int64_t)cur.e.nt * upb) {
+      start += (int64_t)cur.e.nt * upb;
+      cur.e = extent(a, ++cur.b);
+    }
+    cur.uk = (int)quotient(r0 - start, cur.e.nt);
+    cur.tile = (int)(r0 - start - (int64_t)cur.uk * cur.e.nt);
+    ld = cur;
+    wk.place(ld);
+    int64_t left = r1 - r0;  // tiles not yet issued
+#pragma unroll
+    for (int s = 0; s < C::kStages - 1; ++s) {
+      if (left > 0) {
+        wk.issue(ld, s);
+        if (--left) wk.advance(ld);
+      }
+      cp_commit();
+    }
+    seg_from = cur.tile;
+    wk.begin(cur);
+    open = true;
+    int st = 0;
+    for (int64_t i = r0; i < r1; ++i) {
+      cp_wait<C::kStages - 2>();
+      __syncwarp();
+      if (left > 0) {  // the stage read in the last step
+        wk.issue(ld, st == 0 ? C::kStages - 1 : st - 1);
+        if (--left) wk.advance(ld);
+      }
+      cp_commit();
+      wk.step(cur, st);
+      if (++st == C::kStages) st = 0;
+      if (cur.tile + 1 == cur.e.nt) {  // the unit's last tile
+        wk.finish();
+        if (seg_from == 0) {
+          wk.write_out(cur);
+        } else if (i + 1 < r1) {       // begun by another warp: leave the piece for the merge
+          const int hb = cur.uk % a.HB;
+          wk.write_piece(a.head + gw * a.GB * kRow, min(a.GB, a.G - hb * a.GB));
+          if (lane == 0) {
+            s_pb[2 * w] = cur.b, s_uk[2 * w] = cur.uk, s_from[2 * w] = seg_from, s_to[2 * w] = cur.e.nt;
+            s_nt[2 * w] = cur.e.nt, s_tile0[2 * w] = r0;
+          }
+        }
+        open = seg_from != 0 && i + 1 == r1;
+        if (i + 1 < r1) {
+          cur.tile = 0;
+          if (++cur.uk == upb) {
+            cur.uk = 0;
+            do {
+              cur.e = extent(a, ++cur.b);
+            } while (cur.e.nt == 0);
+          }
+          seg_from = 0;
+          wk.begin(cur);
+          open = true;
+        }
+      } else if (i + 1 < r1) {
+        ++cur.tile;
+      } else {
+        wk.finish();
+      }
+    }
+  }
+  cp_wait<0>();
+  __syncthreads();  // every ring is idle: its memory holds the last pieces from here on
+  float* pieces = reinterpret_cast<float*>(smem);
+  if (open) {
+    const int hb = cur.uk % a.HB;
+    wk.write_piece(pieces + w * a.GB * kRow, min(a.GB, a.G - hb * a.GB));
+    if (lane == 0) {
+      const int i = 2 * w + 1;
+      s_pb[i] = cur.b, s_uk[i] = cur.uk, s_from[i] = seg_from, s_to[i] = cur.tile + 1, s_nt[i] = cur.e.nt;
+      s_tile0[i] = r1 - (cur.tile + 1 - seg_from);
+    }
+  }
+  __syncthreads();
+
+  // merge runs of pieces of one unit, in token order
+  for (int i = 0; i < 2 * W;) {
+    if (s_pb[i] < 0) {
+      ++i;
+      continue;
+    }
+    int last = i;
+    for (int j = i + 1; j < 2 * W; ++j) {
+      if (s_pb[j] < 0) continue;
+      if (s_pb[j] != s_pb[i] || s_uk[j] != s_uk[i]) break;
+      last = j;
+    }
+    const int b = s_pb[i], uk = s_uk[i], kvh = uk / a.HB, hb = uk - kvh * a.HB;
+    const int heads = min(a.GB, a.G - hb * a.GB);
+    const bool whole = s_from[i] == 0 && s_to[last] == s_nt[i];
+    const int64_t row0 = (int64_t)b * a.hq + kvh * a.G + hb * a.GB;
+    float* part = a.part + (int64_t)(2 * k + (s_tile0[i] == cta0 ? 0 : 1)) * a.GB * kRow;
+    for (int x = tid; x < heads * (HD / 4); x += NT) {
+      const int h = x / (HD / 4), d0 = (x % (HD / 4)) * 4;
+      float mx = kNegHuge;
+      for (int j = i; j <= last; ++j)
+        if (s_pb[j] >= 0) {
+          const float* pc = (j & 1 ? pieces + (j >> 1) * a.GB * kRow
+                                   : a.head + ((int64_t)k * W + (j >> 1)) * a.GB * kRow) + h * kRow;
+          mx = fmaxf(mx, pc[HD]);
+        }
+      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+      float ls = 0.f;
+      for (int j = i; j <= last; ++j)
+        if (s_pb[j] >= 0) {
+          const float* pc = (j & 1 ? pieces + (j >> 1) * a.GB * kRow
+                                   : a.head + ((int64_t)k * W + (j >> 1)) * a.GB * kRow) + h * kRow;
+          const float f = ex2(pc[HD] - mx);
+          const float4 v = *reinterpret_cast<const float4*>(pc + d0);
+          ls = fmaf(f, pc[HD + 1], ls);
+          o.x = fmaf(f, v.x, o.x), o.y = fmaf(f, v.y, o.y), o.z = fmaf(f, v.z, o.z), o.w = fmaf(f, v.w, o.w);
+        }
+      if (whole) {
+        const float inv = ls == 0.f ? 0.f : 1.f / ls;
+        store4(a, std::is_same<T, __half>::value, (row0 + h) * HD + d0,
+               make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv));
+        if (a.lse && d0 == 0) a.lse[row0 + h] = (mx + log2f(ls)) * kLn2;
+      } else {
+        *reinterpret_cast<float4*>(part + h * kRow + d0) = o;
+        if (d0 == 0) *reinterpret_cast<float2*>(part + h * kRow + HD) = make_float2(mx, ls);
+      }
+    }
+    if (!whole && s_from[i] == 0 && tid == 0) {  // begun here, ended by a later CTA
+      const int64_t end = s_tile0[i] + s_nt[i];
+      a.meta[k] = make_int4(b, uk, (int)((end * n - 1) / total), 1 + (s_tile0[i] == cta0 ? 0 : 1));
+    }
+    i = last + 1;
+  }
+}
+
+// Merge the partials of the unit that CTA blockIdx.x began and others went on with, in CTA
+// order; blockIdx.y: the head. kGroups groups of HD / 4 threads take every kGroups-th partial.
+template <int HD>
+__global__ void __launch_bounds__(256) kv_combine_kernel(const DecArgs a, int f16) {
+  constexpr int kRow = HD + 4, kLanes = HD / 4, kGroups = 256 / kLanes;
+  __shared__ float4 s_o[kGroups][kLanes];
+  __shared__ float s_m[kGroups], s_l[kGroups];
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int k0 = blockIdx.x, h = blockIdx.y;
+  const int4 mt = a.meta[k0];
+  if (!mt.w) return;
+  const int kvh = mt.y / a.HB, hb = mt.y - kvh * a.HB;
+  if (h >= a.G - hb * a.GB) return;
+  const int g = threadIdx.x / kLanes, x = threadIdx.x % kLanes, count = mt.z - k0 + 1;
+  auto row = [&](int i) {
+    const int slot = i == 0 ? 2 * k0 + mt.w - 1 : 2 * (k0 + i);
+    return a.part + ((int64_t)slot * a.GB + h) * kRow;
+  };
+  float m = kNegHuge, l = 0.f;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int i = g; i < count; i += kGroups) m = fmaxf(m, row(i)[HD]);
+#pragma unroll 4
+  for (int i = g; i < count; i += kGroups) {
+    const float* p = row(i);
+    const float f = ex2(p[HD] - m);
+    const float4 v = *reinterpret_cast<const float4*>(p + 4 * x);
+    l = fmaf(f, p[HD + 1], l);
+    o.x = fmaf(f, v.x, o.x), o.y = fmaf(f, v.y, o.y), o.z = fmaf(f, v.z, o.z), o.w = fmaf(f, v.w, o.w);
+  }
+  s_o[g][x] = o;
+  if (x == 0) s_m[g] = m, s_l[g] = l;
+  __syncthreads();
+  if (g) return;
+  float mx = kNegHuge;
+#pragma unroll
+  for (int i = 0; i < kGroups; ++i) mx = fmaxf(mx, s_m[i]);
+  l = 0.f;
+  o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+  for (int i = 0; i < kGroups; ++i) {
+    const float f = ex2(s_m[i] - mx);
+    const float4 v = s_o[i][x];
+    l = fmaf(f, s_l[i], l);
+    o.x = fmaf(f, v.x, o.x), o.y = fmaf(f, v.y, o.y), o.z = fmaf(f, v.z, o.z), o.w = fmaf(f, v.w, o.w);
+  }
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  const int64_t r = (int64_t)mt.x * a.hq + kvh * a.G + hb * a.GB + h;
+  store4(a, f16, r * HD + 4 * x, make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv));
+  if (a.lse && x == 0) a.lse[r] = (mx + log2f(l)) * kLn2;
+}
+
+template <typename T, int FMT, int HD, bool SMALL, bool WHOLE>
+cudaError_t run(const DecArgs& a, int ctas, cudaStream_t st) {
+  using C = Config<FMT, HD>;
+  auto kern = kv_decode_kernel<T, FMT, HD, SMALL, WHOLE>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+  if (e != cudaSuccess) return e;
+  kern<<<ctas, C::kWarps * 32, C::kSmem, st>>>(a);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(ctas, a.GB);
+  cfg.blockDim = dim3(256);
+  cfg.stream = st;
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kv_combine_kernel<HD>, a, (int)std::is_same<T, __half>::value);
+}
+
+template <typename T, int FMT, int HD>
+cudaError_t pick(const DecArgs& a, int ctas, cudaStream_t st) {
+  const bool whole = a.pg.page_size % kTile == 0;
+  if (a.GB <= 4) return whole ? run<T, FMT, HD, true, true>(a, ctas, st) : run<T, FMT, HD, true, false>(a, ctas, st);
+  return whole ? run<T, FMT, HD, false, true>(a, ctas, st) : run<T, FMT, HD, false, false>(a, ctas, st);
+}
+
+template <typename T, int FMT>
+cudaError_t pick_d(int d, const DecArgs& a, int ctas, cudaStream_t st) {
+  if (d == 64) return pick<T, FMT, 64>(a, ctas, st);
+  if (d == 128) return pick<T, FMT, 128>(a, ctas, st);
+  return pick<T, FMT, 256>(a, ctas, st);
+}
+
+constexpr int kMostWarps = 16;
+
+}  // namespace
+
+// Head pieces of every warp, two partials per CTA, the CTAs' records.
+size_t kv_decode_workspace(const tq_ctx* ctx, int G) {
+  const int HB = (G + 7) / 8, GB = (G + HB - 1) / HB;
+  const size_t row = (size_t)GB * (ctx->shape.d + 4) * sizeof(float);
+  return (size_t)ctx->num_sms * ((kMostWarps + 2) * row + sizeof(int4));
+}
+
+cudaError_t launch_kv_decode(const tq_ctx* ctx, const PageView& pg, int format, const void* q, int64_t q_stride,
+                             int batch, int hq, const int32_t* table, int64_t max_pages, const int32_t* seq_lens,
+                             int64_t max_len, int64_t window, float scale, void* out, int out_f32, float* lse,
+                             void* workspace, cudaStream_t stream) {
+  DecArgs a{};
+  a.pg = pg;
+  a.q = static_cast<const char*>(q), a.q_b = q_stride * 2;
+  a.batch = batch, a.hq = hq, a.G = hq / pg.hkv;
+  a.HB = (a.G + 7) / 8, a.GB = (a.G + a.HB - 1) / a.HB;
+  a.table = table, a.max_pages = max_pages, a.lens = seq_lens, a.max_len = max_len;
+  a.window = window, a.scale_log2 = scale * 1.4426950408889634f;
+  a.out = static_cast<char*>(out), a.out_f32 = out_f32, a.lse = lse, a.err = ctx->d_err;
+  const int ctas = ctx->num_sms;
+  const size_t row = (size_t)a.GB * (ctx->shape.d + 4);
+  a.meta = static_cast<int4*>(workspace);
+  a.part = reinterpret_cast<float*>(a.meta + ctas);
+  a.head = a.part + 2 * ctas * row;
+  const int d = ctx->shape.d;
+  if (format == TQ_KV_MXFP4) return pick_d<__nv_bfloat16, TQ_KV_MXFP4>(d, a, ctas, stream);
+  if (format == TQ_KV_BF16) return pick_d<__nv_bfloat16, TQ_KV_BF16>(d, a, ctas, stream);
+  return pick_d<__half, TQ_KV_F16>(d, a, ctas, stream);
+}
+
+}  // namespace tq

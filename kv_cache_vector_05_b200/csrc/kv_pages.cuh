@@ -33,6 +33,11 @@ struct Half2<__nv_bfloat16> {
     const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
     return *reinterpret_cast<const uint32_t*>(&h);
   }
+  static __device__ __forceinline__ uint32_t pack_rz(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rz.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+  }
 };
 template <>
 struct Half2<__half> {
@@ -42,6 +47,11 @@ struct Half2<__half> {
   static __device__ __forceinline__ uint32_t pack(float lo, float hi) {
     const __half2 h = __floats2half2_rn(lo, hi);
     return *reinterpret_cast<const uint32_t*>(&h);
+  }
+  static __device__ __forceinline__ uint32_t pack_rz(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rz.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
   }
 };
 
@@ -66,5 +76,8 @@ __device__ __forceinline__ void e2m1x8_f16(uint32_t w, uint32_t (&out)[4]) {
 __device__ __forceinline__ float e8m0(uint32_t s) {
   return __uint_as_float(s == 0 ? 0x00400000u : s == 255 ? 0x7fffffffu : s << 23);
 }
+
+// The same as bf16 bits.
+__device__ __forceinline__ uint32_t e8m0_bf16(uint32_t s) { return s == 0 ? 0x0040u : s == 255 ? 0x7fffu : s << 7; }
 
 }  // namespace tq

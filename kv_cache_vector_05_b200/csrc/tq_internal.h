@@ -151,7 +151,7 @@ cudaError_t launch_decompress(const tq_ctx* ctx, const uint8_t* k_codes, const u
                               const uint16_t* v_params, int64_t n_vec, float* k_out, float* v_out,
                               cudaStream_t stream);
 
-// ---- page caches (kv_append.cu) ----
+// ---- page caches (kv_append.cu, kv_decode.cu) ----
 
 // Bits of the device error word: a slot, page, position or row range out of bounds.
 constexpr unsigned kErrIndex = 4u;
@@ -175,6 +175,13 @@ cudaError_t launch_kv_append(const tq_ctx* ctx, const PageView& pg, int format, 
                              int64_t q_out_stride, cudaStream_t stream);
 cudaError_t launch_kv_read(const tq_ctx* ctx, const PageView& pg, int format, int64_t n, const int64_t* slot,
                            void* k_out, void* v_out, cudaStream_t stream);
+
+// G: query heads per KV head.
+size_t kv_decode_workspace(const tq_ctx* ctx, int G);
+cudaError_t launch_kv_decode(const tq_ctx* ctx, const PageView& pg, int format, const void* q, int64_t q_stride,
+                             int batch, int hq, const int32_t* table, int64_t max_pages, const int32_t* seq_lens,
+                             int64_t max_len, int64_t window, float scale, void* out, int out_f32, float* lse,
+                             void* workspace, cudaStream_t stream);
 
 // Records the message tq_last_error() returns on this thread (tq_api.cpp).
 void set_last_error(const char* msg);

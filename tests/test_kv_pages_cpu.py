@@ -76,3 +76,37 @@ def test_read_refusals():
     assert lib.tq_read_kv_pages(None, pages(), 3, P, P, P, None) == EINVAL       # no context
     assert "NULL context" in lib.tq_last_error().decode()
     assert lib.tq_read_kv_pages(None, None, 0, None, None, None, None) == OK
+
+
+def decode(pg, q=P, q_dtype=_lib.TQ_BF16, batch=2, hq=4, table=P, max_pages=4, lens=None, max_len=64, window=0,
+           scale=0.0, out=P, out_dtype=_lib.TQ_F32, lse=None, ws=P):
+    return lib.tq_decode_kv_pages(None, pg, q, q_dtype, hq * 128, batch, hq, table, max_pages, lens, max_len, window,
+                                  scale, out, out_dtype, lse, ws, 1 << 20, None)
+
+
+ATTENTION = [
+    (dict(q_dtype=_lib.TQ_F32), EUNSUP, "16-bit"), (dict(q_dtype=_lib.TQ_F16), EUNSUP, "16-bit"),
+    (dict(hq=5), EINVAL, "hq"), (dict(hq=0), EINVAL, "hq"), (dict(q=None), EINVAL, "NULL q"),
+    (dict(out=None), EINVAL, "NULL q or out"), (dict(out=ODD), EINVAL, "out must be 16-byte"),
+    (dict(table=None), EINVAL, "block table"), (dict(table=ODD), EINVAL, "4-byte"), (dict(lens=ODD), EINVAL, "4-byte"),
+    (dict(lse=ODD), EINVAL, "4-byte"), (dict(max_len=-1), EINVAL, "max_len"),
+    (dict(max_len=(1 << 31) - 1), EINVAL, "max_len"), (dict(max_len=65), EINVAL, "max_pages"),
+    (dict(max_pages=-1), EINVAL, "max_pages"), (dict(window=-1), EINVAL, "window"),
+    (dict(scale=float("inf")), EINVAL, "softmax_scale"), (dict(scale=-1.0), EINVAL, "softmax_scale"),
+    (dict(ws=ODD), EINVAL, "workspace"),
+]
+
+
+@pytest.mark.parametrize("kw,status,msg", ATTENTION + [(dict(batch=-1), EINVAL, "batch"),
+                                                       (dict(out_dtype=_lib.TQ_F16), EUNSUP, "out must be fp32"),
+                                                       ({}, EINVAL, "NULL context")])
+def test_decode_refusals(kw, status, msg):
+    assert decode(pages(), **kw) == status and msg in lib.tq_last_error().decode(), lib.tq_last_error()
+
+
+def test_decode_bad_caches_and_empty_batch():
+    for kw, msg in BAD_PAGES:
+        assert decode(pages(**kw)) == EINVAL and msg in lib.tq_last_error().decode()
+    assert decode(None) == EINVAL
+    assert decode(None, q=None, batch=0) == OK
+    assert lib.tq_decode_kv_pages_workspace_bytes(None, 1, 8, 2) == 0
