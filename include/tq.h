@@ -464,6 +464,37 @@ tq_status tq_decode_kv_pages(const tq_ctx* ctx, const tq_kv_pages* pages, const 
                              void* out, tq_dtype out_dtype, float* lse, void* workspace, size_t workspace_bytes,
                              void* stream);
 
+/* Bytes of device workspace tq_prefill_kv_pages needs (may be 0: then workspace may be
+ * NULL). Also 0 for invalid arguments. */
+size_t tq_prefill_kv_pages_workspace_bytes(const tq_ctx* ctx, int64_t total_q, int batch, int hq, int hkv,
+                                           int64_t max_len, int64_t max_q);
+
+/* Causal attention of a chunk of new tokens per sequence over a page cache that already
+ * holds them (tq_append_kv_pages): the whole prompt, a later chunk of it, or several
+ * draft tokens.
+ *   q         device rows [total_q][hq][d] (rows q_stride elements apart, a multiple of 8),
+ *             the sequences' new tokens one after the other
+ *   cu_q      device int32 [batch + 1]: sequence b's rows are cu_q[b] .. cu_q[b + 1] - 1.
+ *             A pair that decreases, leaves [0, total_q] or spans more than max_q rows sets
+ *             the device error word, and that sequence is skipped. Rows of no sequence are
+ *             left as they were.
+ *   max_q     most rows of one sequence
+ *   seq_lens  device int32 [batch]: tokens of each sequence in the cache, the new ones
+ *             included (clamped to [0, max_len]), or NULL for max_len. Sequence b's row i
+ *             of n_b is the token at position seq_len - n_b + i and attends to positions
+ *             up to its own (the newest `window` of them). A row with a negative position
+ *             attends to nothing: zeros and lse = -inf.
+ *   out       device rows [total_q][hq][d] of q_dtype, contiguous; lse NULL or fp32 [total_q][hq]
+ * Probabilities enter the product with the values in q_dtype (the rounding the tensor
+ * cores' operand needs); all sums are fp32. Slots past a sequence's length may hold
+ * anything. A value that is not finite reaches only the rows that attend to it.
+ * Other arguments and errors as tq_decode_kv_pages. */
+tq_status tq_prefill_kv_pages(const tq_ctx* ctx, const tq_kv_pages* pages, const void* q, tq_dtype q_dtype,
+                              int64_t q_stride, int64_t total_q, int batch, int hq, const int32_t* cu_q,
+                              int64_t max_q, const int32_t* block_table, int64_t max_pages,
+                              const int32_t* seq_lens, int64_t max_len, int64_t window, float softmax_scale,
+                              void* out, float* lse, void* workspace, size_t workspace_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

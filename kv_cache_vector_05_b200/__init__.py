@@ -15,4 +15,5 @@ from ._lib import (  # noqa: F401
     TQ_BF16, TQ_ROT_HADAMARD, TQ_ROT_HAAR, TQ_DECODE_AUTO, TQ_DECODE_TCGEN05, TQ_DECODE_MMA, TQ_DECODE_CUDA_CORE,
     DECODE_KERNEL_NAMES, TQ_F16, TQ_KV_BF16, TQ_KV_F16, TQ_KV_MXFP4, KVPages, tq_append_kv_pages,
     tq_read_kv_pages, tq_decode_kv_pages, tq_decode_kv_pages_workspace_bytes,
+    tq_prefill_kv_pages, tq_prefill_kv_pages_workspace_bytes,
 )

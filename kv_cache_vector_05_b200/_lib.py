@@ -29,6 +29,7 @@ EXPORTED = (
     "tq_set_profile_events", "tq_check_device", "tq_decode_attention_static", "tq_decode_static_scratch_capacity",
     "tq_decode_attention_partial", "tq_merge_attention", "tq_set_decode_kernel", "tq_decode_kernel_for",
     "tq_append_kv_pages", "tq_read_kv_pages", "tq_decode_kv_pages_workspace_bytes", "tq_decode_kv_pages",
+    "tq_prefill_kv_pages_workspace_bytes", "tq_prefill_kv_pages",
 )
 
 
@@ -142,6 +143,11 @@ def _load() -> ctypes.CDLL:
     lib.tq_decode_kv_pages.argtypes = [vp, pages, vp, c_int, i64, c_int, c_int, vp, i64, vp, i64, i64,
                                        ctypes.c_float, vp, c_int, vp, vp, sz, vp]
     lib.tq_decode_kv_pages.restype = c_int
+    lib.tq_prefill_kv_pages_workspace_bytes.argtypes = [vp, i64, c_int, c_int, c_int, i64, i64]
+    lib.tq_prefill_kv_pages_workspace_bytes.restype = sz
+    lib.tq_prefill_kv_pages.argtypes = [vp, pages, vp, c_int, i64, i64, c_int, c_int, vp, i64, vp, i64, vp, i64, i64,
+                                        ctypes.c_float, vp, vp, vp, sz, vp]
+    lib.tq_prefill_kv_pages.restype = c_int
     return lib
 
 
@@ -667,4 +673,44 @@ def tq_decode_kv_pages(ctx: Context, q, pages: KVPages, hkv: int, block_table, m
         ctx.handle, p, _ptr(q), _dtype_code(q.dtype), qs, batch, hq, _ptr(block_table), block_table.shape[-1],
         _ptr(seq_lens), max_len, window, softmax_scale, _ptr(out), _dtype_code(out.dtype), _ptr(lse),
         _ptr(workspace), workspace.numel() * workspace.element_size(), _stream(stream)), "tq_decode_kv_pages")
+    return out, lse
+
+
+def tq_prefill_kv_pages_workspace_bytes(ctx: Context, total_q: int, batch: int, hq: int, hkv: int, max_len: int,
+                                        max_q: int) -> int:
+    return int(lib.tq_prefill_kv_pages_workspace_bytes(ctx.handle, total_q, batch, hq, hkv, max_len, max_q))
+
+
+def tq_prefill_kv_pages(ctx: Context, q, pages: KVPages, hkv: int, block_table, max_len: int, cu_q, max_q: int,
+                        seq_lens=None, window: int = 0, softmax_scale: float = 0.0, out=None, lse=None,
+                        workspace=None, stream=None):
+    """Causal attention of the sequences' newest tokens, q [total_q, hq, d] (sequence b's rows are
+    cu_q[b] .. cu_q[b + 1] - 1, int32 [batch + 1]; at most max_q each), over the page cache that
+    already holds them: seq_lens (int32 [batch], or max_len) counts the new tokens too. Other
+    arguments as tq_decode_kv_pages. Returns (out of q's type, lse [total_q, hq] fp32); rows of no
+    sequence keep what out and lse held."""
+    import torch
+    total_q, hq, batch = q.shape[0], q.shape[1], cu_q.shape[0] - 1
+    p = pages.struct(ctx, hkv)
+    qs = _rows(q, "q", total_q, ctx.d, pages)
+    _index(cu_q, "cu_q", torch.int32, (batch + 1,), pages)
+    _table(block_table, batch, hkv, pages)
+    if seq_lens is not None:
+        _index(seq_lens, "seq_lens", torch.int32, (batch,), pages)
+    if out is None:
+        out = torch.empty((total_q, hq, ctx.d), dtype=q.dtype, device=q.device)
+    else:
+        _index(out, "out", q.dtype, (total_q, hq, ctx.d), pages)
+    if lse is None:
+        lse = torch.empty((total_q, hq), dtype=torch.float32, device=q.device)
+    else:
+        _index(lse, "lse", torch.float32, (total_q, hq), pages)
+    need = 0
+    if workspace is None:
+        need = lib.tq_prefill_kv_pages_workspace_bytes(ctx.handle, total_q, batch, hq, hkv, max_len, max_q)
+    workspace = _workspace(workspace, need, q.device)
+    _check(lib.tq_prefill_kv_pages(
+        ctx.handle, p, _ptr(q), _dtype_code(q.dtype), qs, total_q, batch, hq, _ptr(cu_q), max_q, _ptr(block_table),
+        block_table.shape[-1], _ptr(seq_lens), max_len, window, softmax_scale, _ptr(out), _ptr(lse),
+        _ptr(workspace), workspace.numel() * workspace.element_size(), _stream(stream)), "tq_prefill_kv_pages")
     return out, lse

@@ -216,4 +216,40 @@ tq_status tq_decode_kv_pages(const tq_ctx* c, const tq_kv_pages* pages, const vo
   return e == cudaSuccess ? TQ_OK : fail_cuda(e, fn);
 }
 
+size_t tq_prefill_kv_pages_workspace_bytes(const tq_ctx* c, int64_t total_q, int batch, int hq, int hkv,
+                                           int64_t max_len, int64_t max_q) {
+  if (!c || total_q < 0 || batch < 0 || hq <= 0 || hkv <= 0 || hq % hkv || max_len < 0 || max_q < 0) return 0;
+  if (total_q > kMaxRows || max_q > kMaxRows) return 0;
+  if (max_q > total_q) max_q = total_q;
+  return tq::kv_prefill_workspace(c, total_q, batch, hq, hkv, max_len, max_q);
+}
+
+tq_status tq_prefill_kv_pages(const tq_ctx* c, const tq_kv_pages* pages, const void* q, tq_dtype q_dtype,
+                              int64_t q_stride, int64_t total_q, int batch, int hq, const int32_t* cu_q,
+                              int64_t max_q, const int32_t* block_table, int64_t max_pages,
+                              const int32_t* seq_lens, int64_t max_len, int64_t window, float softmax_scale,
+                              void* out, float* lse, void* workspace, size_t workspace_bytes, void* stream) {
+  const char* fn = "tq_prefill_kv_pages";
+  if (batch < 0 || total_q < 0 || max_q < 0) return fail(TQ_EINVAL, fn, "negative batch, total_q or max_q");
+  if (batch == 0 || total_q == 0 || max_q == 0) return TQ_OK;
+  tq_status st = check_attention(fn, pages, q, q_dtype, batch, hq, block_table, max_pages, seq_lens, max_len, window,
+                                 softmax_scale, out, lse, workspace);
+  if (st != TQ_OK) return st;
+  if (!cu_q || !aligned(cu_q, 4)) return fail(TQ_EINVAL, fn, "cu_q must be given and 4-byte aligned");
+  if (total_q > 0x7fffffff) return fail(TQ_EINVAL, fn, "total_q out of range");
+  if (max_q > total_q) max_q = total_q;  // no valid sequence is longer
+  if (max_q * (hq / pages->hkv) > (1 << 30)) return fail(TQ_EUNSUPPORTED, fn, "max_q * hq / hkv above 2^30");
+  tq::PageView w;
+  if ((st = view_pages(fn, c, pages, w)) != TQ_OK) return st;
+  if (!rows_ok(q, q_stride, (int64_t)hq * c->shape.d, total_q))
+    return fail(TQ_EINVAL, fn, "q rows must be 16-byte aligned, q_stride a multiple of 8 and at least a row");
+  const size_t need = tq::kv_prefill_workspace(c, total_q, batch, hq, pages->hkv, max_len, max_q);
+  if (need && (!workspace || workspace_bytes < need)) return fail(TQ_EINVAL, fn, "workspace missing or too small");
+  cudaError_t e = tq::launch_kv_prefill(c, w, (int)pages->format, q, q_stride, total_q, batch, hq, cu_q, max_q,
+                                        block_table, max_pages, seq_lens, max_len, window,
+                                        logit_scale(c, softmax_scale), out, lse, workspace,
+                                        static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? TQ_OK : fail_cuda(e, fn);
+}
+
 }  // extern "C"

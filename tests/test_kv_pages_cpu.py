@@ -110,3 +110,26 @@ def test_decode_bad_caches_and_empty_batch():
     assert decode(None) == EINVAL
     assert decode(None, q=None, batch=0) == OK
     assert lib.tq_decode_kv_pages_workspace_bytes(None, 1, 8, 2) == 0
+
+
+def prefill(pg, q=P, q_dtype=_lib.TQ_BF16, total=10, batch=2, hq=4, cu=P, max_q=8, table=P, max_pages=4, lens=None,
+            max_len=64, window=0, scale=0.0, out=P, lse=None, ws=P):
+    return lib.tq_prefill_kv_pages(None, pg, q, q_dtype, hq * 128, total, batch, hq, cu, max_q, table, max_pages, lens,
+                                   max_len, window, scale, out, lse, ws, 1 << 20, None)
+
+
+@pytest.mark.parametrize("kw,status,msg", ATTENTION + [
+    (dict(batch=-1), EINVAL, "negative"), (dict(total=-1), EINVAL, "negative"), (dict(max_q=-1), EINVAL, "negative"),
+    (dict(cu=None), EINVAL, "cu_q"), (dict(cu=ODD), EINVAL, "cu_q"), (dict(total=1 << 31), EINVAL, "total_q"),
+    (dict(hq=2048, total=1 << 30, max_q=1 << 30), EUNSUP, "2^30"), ({}, EINVAL, "NULL context")])
+def test_prefill_refusals(kw, status, msg):
+    assert prefill(pages(), **kw) == status and msg in lib.tq_last_error().decode(), lib.tq_last_error()
+
+
+def test_prefill_bad_caches_and_nothing_to_do():
+    for kw, msg in BAD_PAGES:
+        assert prefill(pages(**kw)) == EINVAL and msg in lib.tq_last_error().decode()
+    assert prefill(None) == EINVAL
+    for kw in (dict(batch=0), dict(total=0), dict(max_q=0)):
+        assert prefill(None, q=None, **kw) == OK
+    assert lib.tq_prefill_kv_pages_workspace_bytes(None, 1, 1, 4, 2, 10, 1) == 0
