@@ -477,7 +477,7 @@ struct Worker {
       for (int j = 0; j < 2; ++j) {
 #pragma unroll
         for (int o = 4; o < 32; o <<= 1) n[j] = fmaxf(n[j], __shfl_xor_sync(kFull, n[j], o));
-        n[j] = fmaxf(n[j] - kOff, m[j]);
+        n[j] = n[j] > m[j] + (kOff + kSlack) ? n[j] - kOff : m[j];  // a head moves by its own logits alone
         const float f = ex2(m[j] - n[j]);
         m[j] = n[j];
         l[j] *= f;

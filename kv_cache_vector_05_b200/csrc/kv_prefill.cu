@@ -9,15 +9,17 @@
 // tokens, are launched first. Short chunks over long caches leave SMs idle; then the tokens are
 // split as well and combine_kernel joins the parts.
 //
-// One CTA of 12 warps per SM, in roles:
+// One CTA of 12 (MXFP4: 16) warps per SM, in roles:
 //   warps 0-3, 4-7  softmax of row tile 0, 1: thread = row = tensor-memory lane. S is read into
 //                   registers, P = 2^(S' - m) written over it in 16 bits; while one tile's
 //                   exponentials run, the tensor cores work for the other tile
 //   warp 8          one thread issues the MMAs: S = Q K^T (both from shared memory, K-major), then
 //                   O += P V with P from tensor memory and V as it lies in the cache (MN-major)
-//   warps 9-11      bring K and V tiles into a ring of stages in the 128-byte-swizzled layout, by
-//                   cp.async (pages of any size, records of any stride), or, for MXFP4, by loads
-//                   one tile ahead that are turned into exact bf16 values on the way
+//   warps 9 and up  bring K and V tiles into a ring of stages in the 128-byte-swizzled layout:
+//                   pages of whole 8-token groups by TMA, one box per page and 64 columns (warp 9;
+//                   10 and 11 look after edge tiles, below); other pages by cp.async (issuing
+//                   these takes 3 warps three times as long as a tile's products); MXFP4 by loads
+//                   one tile ahead that 7 warps turn into exact bf16 values on the way
 // The accumulated O lives in tensor memory and is rescaled only when a row's maximum has grown
 // by more than 2^kSlack, so almost every tile leaves it alone.
 //
@@ -26,6 +28,10 @@
 // rows differ in what they see (the diagonal, the window's edge) the producers replace such
 // values by 0 and raise a flag; the epilogue then adds them to the rows that do see them.
 #include <algorithm>
+
+#include <cuda.h>  // CUtensorMap and its enums (types only: the encoder is fetched at run time)
+
+#include <atomic>
 
 #include "kv_pages.cuh"
 #include "tq_device.cuh"
@@ -36,7 +42,8 @@ namespace {
 
 using namespace sm100;
 
-constexpr int kThreads = 384, kLoaders = 96;
+// How K and V tiles reach shared memory.
+constexpr int kTma = 0, kCopy = 1, kMx = 2;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kNegHuge = -1.7e38f;  // maximum of no logits: finite, so that -inf - m is -inf
 
@@ -59,10 +66,17 @@ struct PreArgs {
   int splits;
   int blocks;     // row blocks of the longest sequence
   unsigned int* err;
+  int box;        // kTma: tokens per box, a divisor of the page size and of a tile
+  CUtensorMap kmap, vmap;  // kTma: [n_pages][hkv][page_size][d], boxes of `box` tokens x 64 columns
 };
 
-template <bool MX, int HD>
+template <int MODE, int HD>
 struct Config {
+  static constexpr bool MX = MODE == kMx;
+  static constexpr int kThreads = MX ? 512 : 384, kLoaders = kThreads - 288;
+  // registers per thread: launched with kThreads * kLaunch, then moved to the softmax warps:
+  // 384: 256 * 216 + 128 * 72 = 384 * 168; 512: 256 * 168 + 256 * 88 = 512 * 128
+  static constexpr int kMore = MX ? 168 : 216, kLess = MX ? 88 : 72;
   static constexpr int NQ = HD == 256 ? 1 : 2;    // row tiles
   static constexpr int BN = HD == 256 ? 64 : 128; // tokens per K / V tile
   static constexpr int kStage = BN * HD * 2;
@@ -71,13 +85,20 @@ struct Config {
   static constexpr int kOffRow = kQ + kStages * kStage;        // int64 [BN] record offsets
   static constexpr int kOffScale = kOffRow + BN * 8;           // int64 [BN] scale offsets (MXFP4)
   static constexpr int kOffBar = kOffScale + (MX ? BN * 8 : 0);
-  static constexpr int kSmem = 1024 + kOffBar + 256;
+  static constexpr int kSmem = 1024 + kOffBar + 512;
   static constexpr int kS = 128, kO = 256;        // tensor-memory columns: S tile t at t * kS, O at kO + t * HD
 };
 
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// Largest of three floats given by their bits.
+__device__ __forceinline__ float max3(uint32_t a, uint32_t b, uint32_t c) {
+  float y;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(__uint_as_float(a)), "f"(__uint_as_float(b)), "f"(__uint_as_float(c)));
   return y;
 }
 
@@ -101,7 +122,10 @@ __device__ __forceinline__ uint4 lds128(uint32_t a) {
                : "memory");
   return v;
 }
-__device__ __forceinline__ void loaders_sync() { asm volatile("bar.sync 1, 96;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void named_sync() {
+  asm volatile("bar.sync 1, %0;" ::"n"(N) : "memory");
+}
 
 // Shared-memory operand of `rows` rows and HD 16-bit columns: byte of the 16-byte chunk ch of a
 // row (panels of 64 columns, chunks permuted within 128 bytes by row % 8).
@@ -153,16 +177,18 @@ __device__ __forceinline__ Block locate(const PreArgs& a, bool report) {
   return w;
 }
 
-template <typename T, bool MX, int HD>
-__global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const PreArgs a) {
-  using C = Config<MX, HD>;
+template <typename T, int MODE, int HD>
+__global__ void __launch_bounds__(Config<MODE, HD>::kThreads, 1) kv_prefill_kernel(const __grid_constant__ PreArgs a) {
+  using C = Config<MODE, HD>;
+  constexpr bool MX = C::MX;
+  constexpr int kLoaders = C::kLoaders;
   constexpr int NQ = C::NQ, BN = C::BN, NS = C::kStages, ROWS = NQ * 128;
   constexpr bool F16 = std::is_same<T, __half>::value;
   // P in f16: the largest p is 2^13 to 2^15, so that small ones keep their bits
   constexpr float kOff = F16 ? 13.f : 0.f, kSlack = F16 ? 2.f : 8.f;
   extern __shared__ unsigned char smem_raw[];
   unsigned char* sm = reinterpret_cast<unsigned char*>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = __shfl_sync(kFull, tid >> 5, 0), lane = tid & 31;
   const Block w = locate<ROWS>(a, tid == 0);
   if (!w.ok || w.first >= w.rows) return;
 
@@ -198,20 +224,28 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const PreArgs a
   uint64_t* bars = reinterpret_cast<uint64_t*>(sm + C::kOffBar);
   uint64_t* b_q = bars;            // Q in shared memory
   uint64_t* b_s = bars + 1;        // [NQ] S of a row tile written (and its last P V done)
-  uint64_t* b_p = bars + 3;        // [NQ] P of a row tile written
-  uint64_t* b_o = bars + 5;        // [NQ] O of a row tile complete
-  uint64_t* b_full = bars + 7;     // [NS]
-  uint64_t* b_free = bars + 7 + NS;
-  volatile uint32_t* ctl = reinterpret_cast<volatile uint32_t*>(bars + 7 + 2 * NS);  // tmem, dirty
+  uint64_t* b_p = bars + 3;        // [NQ][2] halves of P of a row tile written
+  uint64_t* b_o = bars + 7;        // [NQ] O of a row tile complete
+  uint64_t* b_full = bars + 9;     // [NS]
+  uint64_t* b_free = bars + 9 + NS;
+  uint64_t* b_raw = bars + 9 + 2 * NS;  // [NS] kTma: a V tile with an edge has landed
+  volatile uint32_t* ctl = reinterpret_cast<volatile uint32_t*>(bars + 9 + 3 * NS);  // tmem, dirty
   if (warp == 8) {
     tmem_alloc(const_cast<uint32_t*>(ctl), 512);
     tmem_relinquish();
   }
   if (tid == 0) {
     ctl[1] = 0;
-    mbar_init(b_q, kLoaders);
-    for (int t = 0; t < 2; ++t) mbar_init(b_s + t, 1), mbar_init(b_p + t, 128), mbar_init(b_o + t, 1);
-    for (int s = 0; s < NS; ++s) mbar_init(b_full + s, kLoaders), mbar_init(b_free + s, 1);
+    mbar_init(b_q, 256);
+    for (int t = 0; t < 2; ++t) {
+      mbar_init(b_s + t, 1), mbar_init(b_o + t, 1);
+      mbar_init(b_p + 2 * t, 128), mbar_init(b_p + 2 * t + 1, 128);
+    }
+    for (int s = 0; s < NS; ++s) {
+      mbar_init(b_full + s, MODE == kTma ? 1 : kLoaders);
+      mbar_init(b_free + s, 1);
+      mbar_init(b_raw + s, 1);
+    }
     mbar_init_fence();
   }
   fence_before_sync();
@@ -228,212 +262,306 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const PreArgs a
     return good;
   };
 
-  if (warp >= 9 && n_tiles > 0) {
-    // ---- loaders ----------------------------------------------------------------------
-    const int lt = tid - 288;
-    constexpr int QC = HD / 8, QR = kLoaders / QC;  // 16-byte chunks per row, rows per pass
-    {
-      const int ch = lt % QC;
-      for (int i = lt / QC; i < ROWS; i += QR) {
-        const int row = w.first + i, tok = row / a.G, h = row - tok * a.G;
-        const bool ok = row < end_row;
-        const char* src = a.q + (ok ? (w.q0 + tok) * a.q_b + ((int64_t)w.kvh * a.G + h) * (HD * 2) : 0) + ch * 16;
-        cp_async16(s_q + (i >> 7) * (128 * HD * 2) + chunk_at<128>(i & 127, ch), src, ok);
-      }
-      cp_commit();
-    }
-    // record offsets of a tile's tokens: table entries are loaded a tile ahead of their use
-    int64_t* offs = reinterpret_cast<int64_t*>(sm + C::kOffRow);
-    [[maybe_unused]] int64_t* soffs = reinterpret_cast<int64_t*>(sm + C::kOffScale);
-    const int32_t* trow = a.table + (a.pg.per_head ? (int64_t)w.b * a.pg.hkv + w.kvh : (int64_t)w.b) * a.max_pages;
-    int pid[2], pof[2];
-    auto look = [&](int tile) {
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        int tok = tile * BN + lt + i * kLoaders;
-        tok = tok < lo ? lo : tok >= hi ? hi - 1 : tok;
-        const int blk = tok / (int)a.pg.page_size;
-        pof[i] = tok - blk * (int)a.pg.page_size;
-        pid[i] = __ldg(trow + blk);
-      }
-    };
-    auto place = [&]() {
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int r = lt + i * kLoaders;
-        if (r >= BN) break;
-        int64_t p = pid[i];
-        if (p < 0 || p >= a.pg.n_pages) {
-          atomicOr(a.err, kErrIndex);
-          p = 0;
-        }
-        offs[r] = p * a.pg.page_b + (int64_t)pof[i] * a.pg.tok_b + (int64_t)w.kvh * a.pg.head_b;
-        if constexpr (MX) soffs[r] = p * a.pg.spage_b + (int64_t)pof[i] * a.pg.stok_b + (int64_t)w.kvh * a.pg.shead_b;
-      }
-    };
-    look(t0);
-    place();
-    loaders_sync();
-    bool dirty = false;
-    if constexpr (!MX) {
-      constexpr int kLag = 2;  // copies of this many stages stay in flight
-      const int ch = lt % QC;
-      // group g: 0 is Q, 1 + 2 j K tile j, 2 + 2 j V tile j; stage (g - 1) % NS
-      auto arrive = [&](int g) {
-        if (g == 0) {
-          fence_async_smem();
-          mbar_arrive(b_q);
-          return;
-        }
-        const int st = (g - 1) % NS, kv0 = (t0 + (g - 1) / 2) * BN;
-        if ((g & 1) == 0 && is_edge(kv0)) {  // this thread's own chunks of a V tile
-          for (int r = lt / QC; r < BN; r += QR) {
-            const uint32_t at = s_ring + st * C::kStage + chunk_at<BN>(r, ch);
-            uint4 x = lds128(at);
-            if (scrub<T>(x)) sts128(at, x), dirty = true;
-          }
-          if (dirty) ctl[1] = 1;
-        }
-        fence_async_smem();
-        mbar_arrive(b_full + st);
-      };
-      const int groups = 1 + 2 * n_tiles;
-      for (int g = 1; g < groups; ++g) {
-        const int j = (g - 1) >> 1, st = (g - 1) % NS;
-        if (g > NS) wait(b_free + st, ((g - 1) / NS - 1) & 1);
-        if ((g & 1) && j + 1 < n_tiles) look(t0 + j + 1);
-        const char* src = ((g & 1) ? a.pg.k : a.pg.v) + ch * 16;
-        const int kv0 = (t0 + j) * BN;
-        if (good)
-          for (int r = lt / QC; r < BN; r += QR)
-            cp_async16(s_ring + st * C::kStage + chunk_at<BN>(r, ch), src + offs[r], kv0 + r >= lo && kv0 + r < hi);
-        cp_commit();
-        if (!(g & 1) && j + 1 < n_tiles) {
-          loaders_sync();  // the offsets have been used
-          place();
-          loaders_sync();
-        }
-        if (g >= kLag) {
-          cp_wait<kLag>();
-          arrive(g - kLag);
-        }
-      }
-      cp_wait<0>();
-      for (int g = groups - kLag; g < groups; ++g) arrive(g);  // groups >= 3
-    } else {
-      cp_wait<0>();
-      fence_async_smem();
-      mbar_arrive(b_q);
-      constexpr int CPR = HD / 32, RS = kLoaders / CPR, NC = (BN + RS - 1) / RS;  // one chunk = one block of 32
-      const int blk = lt % CPR, r0 = lt / CPR;
-      uint4 code[NC];
-      uint32_t sc[NC];
-      auto fetch = [&](bool keys, int kv0) {
-#pragma unroll
-        for (int i = 0; i < NC; ++i) {
-          const int r = r0 + i * RS;
-          code[i] = make_uint4(0, 0, 0, 0);
-          sc[i] = 127;
-          if (r < BN && kv0 + r >= lo && kv0 + r < hi) {
-            code[i] = __ldg(reinterpret_cast<const uint4*>((keys ? a.pg.k : a.pg.v) + offs[r] + blk * 16));
-            sc[i] = __ldg((keys ? a.pg.ks : a.pg.vs) + soffs[r] + blk);
-          }
-        }
-      };
-      fetch(true, t0 * BN);
-      for (int h = 0; h < 2 * n_tiles; ++h) {  // K and V tiles in turn
-        const int st = h % NS, kv0 = (t0 + (h >> 1)) * BN;
-        const bool scan = (h & 1) && is_edge(kv0);
-        uint4 cur[NC];
-        uint32_t cs[NC];
-#pragma unroll
-        for (int i = 0; i < NC; ++i) cur[i] = code[i], cs[i] = sc[i];
-        if (!(h & 1)) {
-          fetch(false, kv0);
-          if (h + 2 < 2 * n_tiles) look(t0 + (h >> 1) + 1);
-        } else if (h + 1 < 2 * n_tiles) {
-          loaders_sync();
-          place();
-          loaders_sync();
-          fetch(true, kv0 + BN);
-        }
-        if (h >= NS) wait(b_free + st, (h / NS - 1) & 1);
-#pragma unroll
-        for (int i = 0; i < NC; ++i) {
-          const int r = r0 + i * RS;
-          if (r >= BN || !good) break;
-          const uint32_t wd[4] = {cur[i].x, cur[i].y, cur[i].z, cur[i].w};
-          const uint32_t f = e8m0_bf16(cs[i]) * 0x10001u, two112 = 0x77807780u;
-          const __nv_bfloat162 f2 = *reinterpret_cast<const __nv_bfloat162*>(&f);
-          const __nv_bfloat162 k2 = *reinterpret_cast<const __nv_bfloat162*>(&two112);
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            uint32_t x[4];
-            e2m1x8_f16(wd[c], x);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const uint32_t y = (x[e] & 0x80008000u) | ((x[e] >> 3) & 0x0fff0fffu);  // code 2^-112 as bf16
-              const __nv_bfloat162 v = __hmul2(__hmul2(*reinterpret_cast<const __nv_bfloat162*>(&y), k2), f2);
-              x[e] = *reinterpret_cast<const uint32_t*>(&v);
+  constexpr int QC = HD / 8;  // 16-byte chunks per 16-bit row
+  if (warp >= 8) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kLess));
+    if (warp >= 9 && n_tiles > 0) {
+      // ---- loaders --------------------------------------------------------------------
+      const int lt = tid - 288;
+      const int32_t* trow = a.table + (a.pg.per_head ? (int64_t)w.b * a.pg.hkv + w.kvh : (int64_t)w.b) * a.max_pages;
+      if constexpr (MODE == kTma) {
+        if (warp == 9) {
+          // lane c looks up the page of box c a tile ahead; box (c, 64-column panel p) is issued
+          // by lane (c * panels + p) % 32
+          constexpr int NP = HD / 64;
+          const int per_tile = BN / a.box;
+          int pid = 0, off = 0;
+          bool live = false;
+          auto look = [&](int tile) {
+            const int tok = tile * BN + lane * a.box;
+            live = lane < per_tile && tok < hi && tok + a.box > lo;
+            const int blk = live ? tok / (int)a.pg.page_size : 0;
+            off = tok - blk * (int)a.pg.page_size;
+            if (live) pid = __ldg(trow + blk);
+          };
+          look(t0);
+          for (int h = 0; h < 2 * n_tiles; ++h) {
+            const int st = h % NS, kv0 = (t0 + (h >> 1)) * BN;
+            if (!(h & 1)) {
+              if (live && (pid < 0 || pid >= a.pg.n_pages)) {
+                atomicOr(a.err, kErrIndex);
+                pid = 0;
+              }
             }
-            uint4 o = make_uint4(x[0], x[1], x[2], x[3]);
-            if (scan && scrub<T>(o)) dirty = true;
-            sts128(s_ring + st * C::kStage + chunk_at<BN>(r, blk * 4 + c), o);
+            const uint32_t boxes = __ballot_sync(kFull, live);
+            uint64_t* bar = (h & 1) && is_edge(kv0) ? b_raw + st : b_full + st;
+            if (h >= NS) wait(b_free + st, (h / NS - 1) & 1);
+            if (__all_sync(kFull, good)) {
+              if (lane == 0) mbar_expect_tx(bar, __popc(boxes) * a.box * HD * 2);
+              __syncwarp();
+              for (int i0 = 0; i0 < per_tile * NP; i0 += 32) {
+                const int i = i0 + lane, c = (i / NP) & 31, p = i % NP;
+                const int pg = __shfl_sync(kFull, pid, c), of = __shfl_sync(kFull, off, c);
+                if (i < per_tile * NP && (boxes >> c & 1))
+                  tma_load_4d(sm + C::kQ + st * C::kStage + p * (BN * 128) + c * a.box * 128, (h & 1) ? &a.vmap : &a.kmap,
+                              p * 64, of, a.pg.per_head ? 0 : w.kvh, pg, bar);
+              }
+            }
+            if ((h & 1) && h + 1 < 2 * n_tiles) look(t0 + (h >> 1) + 1);
+          }
+        } else {
+          // edge tiles of V: zero what is not finite, and the rows of tokens that no row here sees
+          uint32_t seen = 0;  // parity of each stage's b_raw
+          for (int j = 0; j < n_tiles; ++j) {
+            if (!is_edge((t0 + j) * BN)) continue;
+            const int st = (2 * j + 1) % NS;
+            wait(b_raw + st, (seen >> st) & 1);
+            seen ^= 1u << st;
+            bool dirty = false;
+            if (good)
+              for (int i = lt - 32; i < BN * QC; i += 64) {
+                const uint32_t at = s_ring + st * C::kStage + i * 16;
+                const int tk = (t0 + j) * BN + i / 8 % BN;
+                uint4 x = lds128(at);
+                if (tk < lo || tk >= hi) sts128(at, make_uint4(0, 0, 0, 0));
+                else if (scrub<T>(x)) sts128(at, x), dirty = true;
+              }
+            if (dirty) ctl[1] = 1;
+            fence_async_smem();
+            named_sync<64>();
+            if (lt == 32) mbar_arrive(b_full + st);
           }
         }
-        if (dirty) ctl[1] = 1;
-        fence_async_smem();
-        mbar_arrive(b_full + st);
+      } else {
+        // record offsets of a tile's tokens: table entries are loaded a tile ahead of their use
+        constexpr int PT = (BN + kLoaders - 1) / kLoaders;
+        int64_t* offs = reinterpret_cast<int64_t*>(sm + C::kOffRow);
+        [[maybe_unused]] int64_t* soffs = reinterpret_cast<int64_t*>(sm + C::kOffScale);
+        int pid[PT], pof[PT];
+        auto look = [&](int tile) {
+#pragma unroll
+          for (int i = 0; i < PT; ++i) {
+            int tok = tile * BN + lt + i * kLoaders;
+            tok = tok < lo ? lo : tok >= hi ? hi - 1 : tok;
+            const int blk = tok / (int)a.pg.page_size;
+            pof[i] = tok - blk * (int)a.pg.page_size;
+            pid[i] = __ldg(trow + blk);
+          }
+        };
+        auto place = [&]() {
+#pragma unroll
+          for (int i = 0; i < PT; ++i) {
+            const int r = lt + i * kLoaders;
+            if (r >= BN) break;
+            int64_t p = pid[i];
+            if (p < 0 || p >= a.pg.n_pages) {
+              atomicOr(a.err, kErrIndex);
+              p = 0;
+            }
+            offs[r] = p * a.pg.page_b + (int64_t)pof[i] * a.pg.tok_b + (int64_t)w.kvh * a.pg.head_b;
+            if constexpr (MX)
+              soffs[r] = p * a.pg.spage_b + (int64_t)pof[i] * a.pg.stok_b + (int64_t)w.kvh * a.pg.shead_b;
+          }
+        };
+        look(t0);
+        place();
+        named_sync<kLoaders>();
+        bool dirty = false;
+        if constexpr (MODE == kCopy) {
+          constexpr int kLag = 2;             // copies of this many stages stay in flight
+          constexpr int QR = kLoaders / QC;   // rows per pass
+          const int ch = lt % QC;
+          // half tile h: K tile h / 2 if even, V tile h / 2 if odd; stage h % NS
+          auto arrive = [&](int h) {
+            const int st = h % NS, kv0 = (t0 + (h >> 1)) * BN;
+            if ((h & 1) && is_edge(kv0)) {    // this thread's own chunks of a V tile
+              for (int r = lt / QC; r < BN; r += QR) {
+                const uint32_t at = s_ring + st * C::kStage + chunk_at<BN>(r, ch);
+                uint4 x = lds128(at);
+                if (scrub<T>(x)) sts128(at, x), dirty = true;
+              }
+              if (dirty) ctl[1] = 1;
+            }
+            fence_async_smem();
+            mbar_arrive(b_full + st);
+          };
+          for (int h = 0; h < 2 * n_tiles; ++h) {
+            const int st = h % NS, kv0 = (t0 + (h >> 1)) * BN;
+            if (h >= NS) wait(b_free + st, (h / NS - 1) & 1);
+            if (!(h & 1) && h + 2 < 2 * n_tiles) look(t0 + (h >> 1) + 1);
+            const char* src = ((h & 1) ? a.pg.v : a.pg.k) + ch * 16;
+            if (good) {
+#pragma unroll 4
+              for (int r = lt / QC; r < BN; r += QR)
+                cp_async16(s_ring + st * C::kStage + chunk_at<BN>(r, ch), src + offs[r], kv0 + r >= lo && kv0 + r < hi);
+            }
+            cp_commit();
+            if ((h & 1) && h + 1 < 2 * n_tiles) {
+              named_sync<kLoaders>();         // the offsets have been used
+              place();
+              named_sync<kLoaders>();
+            }
+            if (h >= kLag) {
+              cp_wait<kLag>();
+              arrive(h - kLag);
+            }
+          }
+          cp_wait<0>();
+          for (int h = 2 * n_tiles - kLag; h < 2 * n_tiles; ++h) arrive(h);
+        } else {
+          // chunk i of a K / V tile pair: one block of 32 coordinates (16 bytes of codes and a
+          // scale) of a token; K's chunks come first
+          constexpr int CPR = HD / 32, HALF = BN * CPR, NC = (2 * HALF + kLoaders - 1) / kLoaders;
+          uint4 code[NC];
+          uint32_t sc[NC];
+          auto fetch = [&](int kv0) {
+#pragma unroll
+            for (int i = 0; i < NC; ++i) {
+              const int x = lt + i * kLoaders, y = x >= HALF ? x - HALF : x, r = y / CPR, blk = y % CPR;
+              code[i] = make_uint4(0, 0, 0, 0);
+              sc[i] = 127;
+              if (x < 2 * HALF && kv0 + r >= lo && kv0 + r < hi) {
+                code[i] = __ldg(reinterpret_cast<const uint4*>((x < HALF ? a.pg.k : a.pg.v) + offs[r] + blk * 16));
+                sc[i] = __ldg((x < HALF ? a.pg.ks : a.pg.vs) + soffs[r] + blk);
+              }
+            }
+          };
+          fetch(t0 * BN);
+          if (n_tiles > 1) look(t0 + 1);
+          for (int j = 0; j < n_tiles; ++j) {
+            const int sk = (2 * j) % NS, sv = (2 * j + 1) % NS, kv0 = (t0 + j) * BN;
+            const bool edge = is_edge(kv0);
+            uint4 cur[NC];
+            uint32_t cs[NC];
+#pragma unroll
+            for (int i = 0; i < NC; ++i) cur[i] = code[i], cs[i] = sc[i];
+            if (j + 1 < n_tiles) {
+              named_sync<kLoaders>();  // the offsets have been used
+              place();
+              named_sync<kLoaders>();
+              fetch(kv0 + BN);
+              if (j + 2 < n_tiles) look(t0 + j + 2);
+            }
+            if (2 * j >= NS) wait(b_free + sk, (2 * j / NS - 1) & 1);
+            if (2 * j + 1 >= NS) wait(b_free + sv, ((2 * j + 1) / NS - 1) & 1);
+#pragma unroll
+            for (int i = 0; i < NC; ++i) {
+              const int x = lt + i * kLoaders, y = x >= HALF ? x - HALF : x, r = y / CPR, blk = y % CPR;
+              if (x >= 2 * HALF || !good) break;
+              const uint32_t base = s_ring + (x < HALF ? sk : sv) * C::kStage;
+              const uint32_t wd[4] = {cur[i].x, cur[i].y, cur[i].z, cur[i].w};
+              const uint32_t f = e8m0_bf16(cs[i]) * 0x10001u, two112 = 0x77807780u;
+              const __nv_bfloat162 f2 = *reinterpret_cast<const __nv_bfloat162*>(&f);
+              const __nv_bfloat162 k2 = *reinterpret_cast<const __nv_bfloat162*>(&two112);
+#pragma unroll
+              for (int c = 0; c < 4; ++c) {
+                uint32_t v[4];
+                e2m1x8_f16(wd[c], v);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                  const uint32_t z = (v[e] & 0x80008000u) | ((v[e] >> 3) & 0x0fff0fffu);  // code 2^-112 as bf16
+                  const __nv_bfloat162 u = __hmul2(__hmul2(*reinterpret_cast<const __nv_bfloat162*>(&z), k2), f2);
+                  v[e] = *reinterpret_cast<const uint32_t*>(&u);
+                }
+                uint4 o = make_uint4(v[0], v[1], v[2], v[3]);
+                if (edge && x >= HALF && scrub<T>(o)) dirty = true;
+                sts128(base + chunk_at<BN>(r, blk * 4 + c), o);
+              }
+            }
+            if (dirty) ctl[1] = 1;
+            fence_async_smem();
+            mbar_arrive(b_full + sk);
+            mbar_arrive(b_full + sv);
+          }
+        }
       }
-    }
-  } else if (warp == 8 && n_tiles > 0) {
-    // ---- MMA issue ----------------------------------------------------------------------
-    if (lane == 0) {
+    } else if (warp == 8 && n_tiles > 0) {
+      // ---- MMA issue: the whole warp walks the loop, one lane issues ----------------------
       constexpr uint32_t kFmt = F16 ? 0u : 1u;
       constexpr uint32_t i_qk = idesc_f16_f32(128, BN) | (kFmt << 7) | (kFmt << 10);
       constexpr uint32_t i_pv = idesc_f16_f32(128, HD) | (kFmt << 7) | (kFmt << 10) | (1u << 16);  // B MN-major
+      // K-steps are constant offsets of 16-byte units in a descriptor's address field (shared
+      // memory ends below the field's 2^18 bytes, so the sums do not carry)
+      const uint64_t d_q = sw128_desc(s_q, 0, 128), d_k = sw128_desc(s_ring, 0, BN), d_v = sw128_mn_desc(s_ring, 0, BN);
       auto qk = [&](int t, int st) {
+        const uint64_t q = d_q + (uint32_t)(t * (128 * HD * 2 / 16)), k = d_k + (uint32_t)(st * (C::kStage / 16));
+        if (elect_one()) {
 #pragma unroll
-        for (int k = 0; k < HD; k += 16)
-          umma_f16(tmem + t * C::kS, sw128_desc(s_q + t * (128 * HD * 2), k, 128),
-                   sw128_desc(s_ring + st * C::kStage, k, BN), i_qk, k > 0);
-        umma_commit(b_s + t);
+          for (int i = 0; i < HD; i += 16)
+            umma_f16(tmem + t * C::kS, q + (i / 64 * (128 * 128) + i % 64 * 2) / 16,
+                     k + (i / 64 * (BN * 128) + i % 64 * 2) / 16, i_qk, i > 0);
+          umma_commit(b_s + t);
+        }
+        __syncwarp();
       };
-      auto pv = [&](int t, int st, bool acc) {
+      // half of a tile's tokens: P's first columns are multiplied while the others are computed
+      auto pv = [&](int t, int st, int half, bool acc) {
+        const uint64_t v = d_v + (uint32_t)(st * (C::kStage / 16));
+        if (elect_one()) {
 #pragma unroll
-        for (int k = 0; k < BN; k += 16)
-          umma_f16_ts(tmem + C::kO + t * HD, tmem + t * C::kS + k / 2, sw128_mn_desc(s_ring + st * C::kStage, k, BN),
-                      i_pv, acc || k > 0);
+          for (int i = 0; i < BN / 2; i += 16) {
+            const int k = half * (BN / 2) + i;
+            umma_f16_ts(tmem + C::kO + t * HD, tmem + t * C::kS + k / 2, v + k * 128 / 16, i_pv, acc || i > 0);
+          }
+        }
+        __syncwarp();
       };
-      if (wait(b_q, 0) && wait(b_full, 0)) {
+      auto commit = [&](uint64_t* bar) {
+        if (elect_one()) umma_commit(bar);
+        __syncwarp();
+      };
+      auto warp_wait = [&](uint64_t* bar, uint32_t parity) {
+        const bool ok = __all_sync(kFull, wait(bar, parity));
         fence_after_sync();
+        return ok;
+      };
+      if (warp_wait(b_q, 0) && warp_wait(b_full, 0)) {
 #pragma unroll
         for (int t = 0; t < NQ; ++t)
           if (cnt[t] > 0) qk(t, 0);
-        umma_commit(b_free);
-        for (int j = 0; j < n_tiles && good; ++j) {
-          const int sv = (2 * j + 1) % NS, sk = (2 * j + 2) % NS;
-          if (!wait(b_full + sv, ((2 * j + 1) / NS) & 1)) break;
-          if (j + 1 < n_tiles && !wait(b_full + sk, ((2 * j + 2) / NS) & 1)) break;
+        commit(b_free);
+        int sv = 1 % NS, sk = 2 % NS;  // stages of V tile j and K tile j + 1
+        uint32_t v_par = 0, k_par = 0;
+        for (int j = 0; j < n_tiles; ++j) {
+          if (!warp_wait(b_full + sv, v_par)) break;
+          if (j + 1 < n_tiles && !warp_wait(b_full + sk, k_par)) break;
+          bool ok = true;
 #pragma unroll
           for (int t = 0; t < NQ; ++t) {
             if (j >= cnt[t]) continue;
-            if (!wait(b_p + t, j & 1)) break;
-            fence_after_sync();
-            pv(t, sv, j > 0);
+            if (!(ok = warp_wait(b_p + 2 * t, j & 1))) break;
+            pv(t, sv, 0, j > 0);
+            if (!(ok = warp_wait(b_p + 2 * t + 1, j & 1))) break;
+            pv(t, sv, 1, true);
             if (j + 1 < cnt[t]) qk(t, sk);
-            else umma_commit(b_o + t);
+            else commit(b_o + t);
           }
-          umma_commit(b_free + sv);
-          if (j + 1 < n_tiles) umma_commit(b_free + sk);
+          if (!ok) break;
+          commit(b_free + sv);
+          if (j + 1 < n_tiles) commit(b_free + sk);
+          if ((sv += 2) >= NS) sv -= NS, v_par ^= 1;
+          if ((sk += 2) >= NS) sk -= NS, k_par ^= 1;
         }
         // the last arrival of a commit must not outlive the block's shared memory
         const int last = 2 * n_tiles - 1;
-        wait(b_free + last % NS, (last / NS) & 1);
+        warp_wait(b_free + last % NS, (last / NS) & 1);
       }
     }
-    __syncwarp();
-  } else if (warp < 4 * NQ) {
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kMore));
+    if (n_tiles > 0) {  // Q, while the loaders start
+      for (int i = tid; i < ROWS * QC; i += 256) {
+        const int rr = i / QC, ch = i % QC, row = w.first + rr, tk = row / a.G, h = row - tk * a.G;
+        const bool ok = row < end_row;
+        const char* src = a.q + (ok ? (w.q0 + tk) * a.q_b + ((int64_t)w.kvh * a.G + h) * (HD * 2) : 0) + ch * 16;
+        cp_async16(s_q + (rr >> 7) * (128 * HD * 2) + chunk_at<128>(rr & 127, ch), src, ok);
+      }
+      cp_commit();
+      cp_wait<0>();
+      fence_async_smem();
+      mbar_arrive(b_q);
+    }
+    if (warp < 4 * NQ) {
     // ---- softmax ------------------------------------------------------------------------
     const int t = warp >> 2, i = w.first + t * 128 + (warp & 3) * 32 + lane;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
@@ -456,13 +584,16 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const PreArgs a
         for (int c = 0; c < BN; ++c)
           if (c > last || c < from) s[c] = 0xff800000u;
       }
-      float mx = __uint_as_float(s[0]), my = __uint_as_float(s[1]);
+      float mx = max3(s[0], s[1], s[2]), my = max3(s[3], s[4], s[5]);
 #pragma unroll
-      for (int c = 2; c < BN; c += 2)
-        mx = fmaxf(mx, __uint_as_float(s[c])), my = fmaxf(my, __uint_as_float(s[c + 1]));
-      mx = fmaxf(mx, my) * sl;
-      if (__any_sync(kFull, mx > m + (kOff + kSlack))) {
-        const float mn = fmaxf(m, mx - kOff), f = ex2(m - mn);
+      for (int c = 6; c + 3 < BN; c += 4) {
+        mx = max3(__float_as_uint(mx), s[c], s[c + 1]);
+        my = max3(__float_as_uint(my), s[c + 2], s[c + 3]);
+      }
+      mx = max3(__float_as_uint(fmaxf(mx, my)), s[BN - 2], s[BN - 1]) * sl;
+      const bool grown = mx > m + (kOff + kSlack);
+      if (__any_sync(kFull, grown)) {  // rows that need none keep their m: f = 1
+        const float mn = grown ? mx - kOff : m, f = ex2(m - mn);
         m = mn;
         l *= f;
         if (j > 0) {
@@ -490,11 +621,13 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const PreArgs a
           pk[e / 2] = Half2<T>::pack(p.x, p.y);
         }
         tmem_st16(ts + c / 2, pk);
+        if (c + 32 == BN / 2 || c + 32 == BN) {
+          tmem_st_wait();
+          fence_before_sync();
+          mbar_arrive(b_p + 2 * t + (c + 32 == BN ? 1 : 0));
+        }
       }
       l += sum.x + sum.y;
-      tmem_st_wait();
-      fence_before_sync();
-      mbar_arrive(b_p + t);
     }
     // epilogue: O / l in q's type, or the parts of a split
     if (n > 0) good = __all_sync(kFull, wait(b_o + t, 0));
@@ -579,6 +712,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const PreArgs a
         else if (a.lse) a.lse[row] = (m + log2f(l)) * kLn2;
       }
     }
+    }
   }
   fence_before_sync();
   __syncthreads();
@@ -587,7 +721,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const PreArgs a
 
 // Join the parts of split rows: one warp per row of the same blocks.
 template <typename T, int HD, int ROWS>
-__global__ void __launch_bounds__(256) kv_prefill_combine_kernel(const PreArgs a) {
+__global__ void __launch_bounds__(256) kv_prefill_combine_kernel(const __grid_constant__ PreArgs a) {
   constexpr int E = HD / 32;  // values per lane
   const Block w = locate<ROWS>(a, false);
   if (!w.ok) return;
@@ -615,25 +749,75 @@ __global__ void __launch_bounds__(256) kv_prefill_combine_kernel(const PreArgs a
   }
 }
 
-template <typename T, bool MX, int HD>
-cudaError_t run(const PreArgs& a, cudaStream_t st) {
-  using C = Config<MX, HD>;
-  auto kern = kv_prefill_kernel<T, MX, HD>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
-  if (e != cudaSuccess) return e;
+// cuTensorMapEncodeTiled, fetched once from the driver through the runtime.
+using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                   const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                   CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+EncodeTiledFn tensor_map_encoder() {
+  static const EncodeTiledFn fn = []() -> EncodeTiledFn {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+      return nullptr;
+    return reinterpret_cast<EncodeTiledFn>(p);
+  }();
+  return fn;
+}
+
+// The pages as a [n_pages][heads][page_size][d] tensor of 16-bit values (of either type: boxes are
+// only copied), in boxes of one page and head, `box` tokens and 64 columns. False where the
+// encoder takes no such strides.
+bool encode_pages(CUtensorMap* map, const void* base, const PageView& pg, int d, int box) {
+  const EncodeTiledFn enc = tensor_map_encoder();
+  if (!enc) return false;
+  const int heads = pg.per_head ? 1 : pg.hkv;
+  const cuuint64_t dims[4] = {(cuuint64_t)d, (cuuint64_t)pg.page_size, (cuuint64_t)heads, (cuuint64_t)pg.n_pages};
+  const cuuint64_t row = (cuuint64_t)d * 2;  // stands in for the stride of a dimension of one
+  const cuuint64_t strides[3] = {pg.page_size > 1 ? (cuuint64_t)pg.tok_b : row, heads > 1 ? (cuuint64_t)pg.head_b : row,
+                                 pg.n_pages > 1 ? (cuuint64_t)pg.page_b : row};
+  const cuuint32_t boxes[4] = {64, (cuuint32_t)box, 1, 1}, estr[4] = {1, 1, 1, 1};
+  for (cuuint64_t s : strides)
+    if (s >= ((cuuint64_t)1 << 40)) return false;
+  return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, boxes, estr,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <typename T, int MODE, int HD>
+cudaError_t run(const PreArgs& a, int device, cudaStream_t st) {
+  using C = Config<MODE, HD>;
+  auto kern = kv_prefill_kernel<T, MODE, HD>;
+  static std::atomic<uint64_t> configured{0};  // devices on which the kernel may use its shared memory
+  cudaError_t e;
+  if (device >= 64 || !(configured.load() >> device & 1)) {
+    if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem)) != cudaSuccess) return e;
+    if (device < 64) configured.fetch_or((uint64_t)1 << device);
+  }
   const int64_t blocks = (int64_t)a.blocks * a.batch * a.pg.hkv;
   if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
-  kern<<<dim3((unsigned)blocks, a.splits), kThreads, C::kSmem, st>>>(a);
+  kern<<<dim3((unsigned)blocks, a.splits), C::kThreads, C::kSmem, st>>>(a);
   if ((e = cudaGetLastError()) != cudaSuccess || a.splits == 1) return e;
   kv_prefill_combine_kernel<T, HD, C::NQ * 128><<<(unsigned)blocks, 256, 0, st>>>(a);
   return cudaGetLastError();
 }
 
-template <typename T, bool MX>
-cudaError_t pick(int d, const PreArgs& a, cudaStream_t st) {
-  if (d == 64) return run<T, MX, 64>(a, st);
-  if (d == 128) return run<T, MX, 128>(a, st);
-  return run<T, MX, 256>(a, st);
+template <typename T, int MODE>
+cudaError_t pick_d(int d, const PreArgs& a, int device, cudaStream_t st) {
+  if (d == 64) return run<T, MODE, 64>(a, device, st);
+  if (d == 128) return run<T, MODE, 128>(a, device, st);
+  return run<T, MODE, 256>(a, device, st);
+}
+
+template <typename T>
+cudaError_t pick(int d, PreArgs& a, int device, cudaStream_t st) {
+  // boxes of whole 8-row swizzle groups that end neither past a page nor past a tile
+  int box = d == 256 ? 64 : 128;
+  while (box >= 8 && a.pg.page_size % box) box /= 2;
+  a.box = box;
+  if (box >= 8 && encode_pages(&a.kmap, a.pg.k, a.pg, d, box) && encode_pages(&a.vmap, a.pg.v, a.pg, d, box))
+    return pick_d<T, kTma>(d, a, device, st);
+  return pick_d<T, kCopy>(d, a, device, st);
 }
 
 int block_rows(int d) { return d == 256 ? 128 : 256; }
@@ -673,9 +857,9 @@ cudaError_t launch_kv_prefill(const tq_ctx* ctx, const PageView& pg, int format,
   const int rows = block_rows(ctx->shape.d);
   a.blocks = (int)((max_q * a.G + rows - 1) / rows);
   const int d = ctx->shape.d;
-  if (format == TQ_KV_MXFP4) return pick<__nv_bfloat16, true>(d, a, stream);
-  if (format == TQ_KV_BF16) return pick<__nv_bfloat16, false>(d, a, stream);
-  return pick<__half, false>(d, a, stream);
+  if (format == TQ_KV_MXFP4) return pick_d<__nv_bfloat16, kMx>(d, a, ctx->device, stream);
+  if (format == TQ_KV_BF16) return pick<__nv_bfloat16>(d, a, ctx->device, stream);
+  return pick<__half>(d, a, ctx->device, stream);
 }
 
 }  // namespace tq

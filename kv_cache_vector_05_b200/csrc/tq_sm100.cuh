@@ -79,6 +79,15 @@ __device__ __forceinline__ void tma_load_2d(void* dst, const void* map, int x, i
       : "memory");
 }
 
+// The same for a 4-D tensor map.
+__device__ __forceinline__ void tma_load_4d(void* dst, const void* map, int x, int y, int z, int w, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], "
+      "[%6];" ::"r"(smem_u32(dst)),
+      "l"(map), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_u32(bar))
+      : "memory");
+}
+
 // Named barrier `id` over `count` threads that also ORs a predicate across them.
 template <int ID, int COUNT>
 __device__ __forceinline__ bool bar_sync_or(bool p) {
@@ -148,6 +157,15 @@ __device__ __forceinline__ void fence_after_sync() {
 // Make generic-proxy writes to shared memory visible to the tensor core.
 __device__ __forceinline__ void fence_async_smem() {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
+
+// True in one lane of a converged warp. An MMA issued under this predicate from warp-uniform
+// code has its descriptors in uniform registers; under a per-thread condition (lane == 0) each
+// one is moved there first, and a 128 x 128 x 16 MMA takes about 158 cycles to issue, not 66.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{ .reg .pred q; elect.sync _|q, 0xffffffff; selp.u32 %0, 1, 0, q; }" : "=r"(p));
+  return p != 0;
 }
 
 // D[tmem] (+)= A[smem] x B[smem], kind::f16, one CTA. `accumulate` = 0 overwrites D.
