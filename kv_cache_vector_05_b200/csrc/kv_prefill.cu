@@ -16,10 +16,10 @@
 //   warp 8          one thread issues the MMAs: S = Q K^T (both from shared memory, K-major), then
 //                   O += P V with P from tensor memory and V as it lies in the cache (MN-major)
 //   warps 9 and up  bring K and V tiles into a ring of stages in the 128-byte-swizzled layout:
-//                   pages of whole 8-token groups by TMA, one box per page and 64 columns (warp 9;
-//                   10 and 11 look after edge tiles, below); other pages by cp.async (issuing
-//                   these takes 3 warps three times as long as a tile's products); MXFP4 by loads
-//                   one tile ahead that 7 warps turn into exact bf16 values on the way
+//                   pages of whole 8-token groups by TMA, one box per page and 64 columns; other
+//                   pages by cp.async (issuing these takes 3 warps three times as long as a
+//                   tile's products); MXFP4 by loads one tile ahead that 7 warps turn into exact
+//                   bf16 values on the way
 // The accumulated O lives in tensor memory and is rescaled only when a row's maximum has grown
 // by more than 2^kSlack, so almost every tile leaves it alone.
 //
@@ -59,6 +59,8 @@ struct PreArgs {
   int64_t max_pages;
   const int32_t* lens;
   int64_t max_len, window;
+  uint32_t g_mul; // row / G = row * g_mul >> g_shift for rows below 2^30
+  int g_shift;
   float scale_log2;
   char* out;
   float* lse;
@@ -148,6 +150,12 @@ __device__ __forceinline__ bool scrub(uint4& x) {
   return any;
 }
 
+// Token of a packed row. With g_mul = ceil(2^k / G), k = 30 + ceil(log2 G), the product is above
+// row 2^k / G by row (g_mul G - 2^k) / G < 2^30: less than 2^k / G, so the quotient is exact.
+__device__ __forceinline__ int token_of(const PreArgs& a, int row) {
+  return (int)((uint64_t)(uint32_t)row * a.g_mul >> a.g_shift);
+}
+
 // What a block works on.
 struct Block {
   int64_t q0;         // first row of the sequence in q
@@ -195,7 +203,7 @@ __global__ void __launch_bounds__(Config<MODE, HD>::kThreads, 1) kv_prefill_kern
   // positions: row i's token sits at p0 + i / G; tokens of this block's rows: [lo, hi)
   const int p0 = w.n - w.nq;
   int end_row = w.first + ROWS < w.rows ? w.first + ROWS : w.rows;
-  const int pmin = p0 + w.first / a.G, pmax = p0 + (end_row - 1) / a.G;
+  const int pmin = p0 + token_of(a, w.first), pmax = p0 + token_of(a, end_row - 1);
   const int wnd = a.window && a.window < 0x7fffffff ? (int)a.window : 0;
   const int lo = wnd && pmin - wnd + 1 > 0 ? pmin - wnd + 1 : 0;
   const int hi = pmax + 1;  // <= n
@@ -213,7 +221,7 @@ __global__ void __launch_bounds__(Config<MODE, HD>::kThreads, 1) kv_prefill_kern
     cnt[t] = 0, tmin[t] = tmax[t] = 0;
     if (t >= NQ || f >= end_row) continue;
     const int l = f + 127 < end_row - 1 ? f + 127 : end_row - 1;
-    tmin[t] = p0 + f / a.G, tmax[t] = p0 + l / a.G;
+    tmin[t] = p0 + token_of(a, f), tmax[t] = p0 + token_of(a, l);
     const int te = tmax[t] < 0 ? t0 : tmax[t] / BN + 1;
     cnt[t] = (te < t1 ? te : t1) - t0;
     if (cnt[t] < 0) cnt[t] = 0;
@@ -221,6 +229,19 @@ __global__ void __launch_bounds__(Config<MODE, HD>::kThreads, 1) kv_prefill_kern
   const int n_tiles = cnt[0] > cnt[1] ? cnt[0] : cnt[1];
   auto is_edge = [&](int kv0) { return kv0 + BN - 1 > pmin || (wnd && kv0 <= pmax - wnd); };
 
+  constexpr int QC = HD / 8;  // 16-byte chunks per 16-bit row
+  const uint32_t s_q = smem_u32(sm), s_ring = s_q + C::kQ;
+  if (warp < 8 && n_tiles > 0) {  // Q is on its way while barriers and tensor memory are set up
+    const int ch = tid % QC;
+#pragma unroll
+    for (int rr = tid / QC; rr < ROWS; rr += 256 / QC) {
+      const int row = w.first + rr, tk = token_of(a, row), h = row - tk * a.G;
+      const bool ok = row < end_row;
+      const char* src = a.q + (ok ? (w.q0 + tk) * a.q_b + ((int64_t)w.kvh * a.G + h) * (HD * 2) : 0) + ch * 16;
+      cp_async16(s_q + (rr >> 7) * (128 * HD * 2) + chunk_at<128>(rr & 127, ch), src, ok);
+    }
+    cp_commit();
+  }
   uint64_t* bars = reinterpret_cast<uint64_t*>(sm + C::kOffBar);
   uint64_t* b_q = bars;            // Q in shared memory
   uint64_t* b_s = bars + 1;        // [NQ] S of a row tile written (and its last P V done)
@@ -230,6 +251,10 @@ __global__ void __launch_bounds__(Config<MODE, HD>::kThreads, 1) kv_prefill_kern
   uint64_t* b_free = bars + 9 + NS;
   uint64_t* b_raw = bars + 9 + 2 * NS;  // [NS] kTma: a V tile with an edge has landed
   volatile uint32_t* ctl = reinterpret_cast<volatile uint32_t*>(bars + 9 + 3 * NS);  // tmem, dirty
+  if (MODE == kTma && tid == 288) {
+    asm volatile("prefetch.tensormap [%0];" ::"l"(&a.kmap) : "memory");
+    asm volatile("prefetch.tensormap [%0];" ::"l"(&a.vmap) : "memory");
+  }
   if (warp == 8) {
     tmem_alloc(const_cast<uint32_t*>(ctl), 512);
     tmem_relinquish();
@@ -252,17 +277,15 @@ __global__ void __launch_bounds__(Config<MODE, HD>::kThreads, 1) kv_prefill_kern
   __syncthreads();
   fence_after_sync();
   const uint32_t tmem = ctl[0];
-  const uint32_t s_q = smem_u32(sm), s_ring = s_q + C::kQ;
   bool good = true;  // no wait has timed out; after one, the roles run out without waiting
   auto wait = [&](uint64_t* bar, uint32_t parity) {
-    if (good && !mbar_wait(bar, parity)) {
+    if (good && !mbar_spin(bar, parity)) {
       good = false;
       atomicOr(a.err, 1u);
     }
     return good;
   };
 
-  constexpr int QC = HD / 8;  // 16-byte chunks per 16-bit row
   if (warp >= 8) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kLess));
     if (warp >= 9 && n_tiles > 0) {
@@ -270,68 +293,68 @@ __global__ void __launch_bounds__(Config<MODE, HD>::kThreads, 1) kv_prefill_kern
       const int lt = tid - 288;
       const int32_t* trow = a.table + (a.pg.per_head ? (int64_t)w.b * a.pg.hkv + w.kvh : (int64_t)w.b) * a.max_pages;
       if constexpr (MODE == kTma) {
-        if (warp == 9) {
-          // lane c looks up the page of box c a tile ahead; box (c, 64-column panel p) is issued
-          // by lane (c * panels + p) % 32
-          constexpr int NP = HD / 64;
-          const int per_tile = BN / a.box;
-          int pid = 0, off = 0;
-          bool live = false;
-          auto look = [&](int tile) {
-            const int tok = tile * BN + lane * a.box;
-            live = lane < per_tile && tok < hi && tok + a.box > lo;
-            const int blk = live ? tok / (int)a.pg.page_size : 0;
-            off = tok - blk * (int)a.pg.page_size;
-            if (live) pid = __ldg(trow + blk);
-          };
-          look(t0);
-          for (int h = 0; h < 2 * n_tiles; ++h) {
-            const int st = h % NS, kv0 = (t0 + (h >> 1)) * BN;
-            if (!(h & 1)) {
-              if (live && (pid < 0 || pid >= a.pg.n_pages)) {
-                atomicOr(a.err, kErrIndex);
-                pid = 0;
-              }
+        // Lane c looks up the page of box c (of both K and V) a tile ahead; box (c, 64-column panel
+        // p) of a tile is issued by warp 9 + (c * panels + p) % 3 (one issue takes a warp about
+        // 100 cycles, since its operands differ from box to box). Warp 9 announces the bytes.
+        constexpr int NP = HD / 64;
+        const int per_tile = BN / a.box, me = warp - 9;
+        int pid = 0, off = 0;
+        bool live = false;
+        auto look = [&](int tile) {
+          const int tok = tile * BN + lane * a.box;
+          live = lane < per_tile && tok < hi && tok + a.box > lo;
+          const int blk = live ? tok / (int)a.pg.page_size : 0;
+          off = tok - blk * (int)a.pg.page_size;
+          if (live) pid = __ldg(trow + blk);
+        };
+        uint32_t seen = 0;  // parity of each stage's b_raw
+        // edge tiles of V: zero what is not finite, and the rows of tokens that no row here sees
+        auto mend = [&](int j) {
+          if (!is_edge((t0 + j) * BN)) return;
+          const int st = (2 * j + 1) % NS;
+          wait(b_raw + st, (seen >> st) & 1);
+          seen ^= 1u << st;
+          bool dirty = false;
+          if (good)
+            for (int i = lt; i < BN * QC; i += kLoaders) {
+              const uint32_t at = s_ring + st * C::kStage + i * 16;
+              const int tk = (t0 + j) * BN + i / 8 % BN;
+              uint4 x = lds128(at);
+              if (tk < lo || tk >= hi) sts128(at, make_uint4(0, 0, 0, 0));
+              else if (scrub<T>(x)) sts128(at, x), dirty = true;
             }
-            const uint32_t boxes = __ballot_sync(kFull, live);
-            uint64_t* bar = (h & 1) && is_edge(kv0) ? b_raw + st : b_full + st;
+          if (dirty) ctl[1] = 1;
+          fence_async_smem();
+          named_sync<kLoaders>();
+          if (lt == 0) mbar_arrive(b_full + st);
+        };
+        look(t0);
+        for (int j = 0; j < n_tiles; ++j) {
+          if (live && (pid < 0 || pid >= a.pg.n_pages)) {
+            if (me == 0) atomicOr(a.err, kErrIndex);
+            pid = 0;
+          }
+          const uint32_t boxes = __ballot_sync(kFull, live);
+          const int pg = pid, of = off;
+          if (j + 1 < n_tiles) look(t0 + j + 1);
+#pragma unroll
+          for (int kv = 0; kv < 2; ++kv) {
+            const int h = 2 * j + kv, st = h % NS;
+            uint64_t* bar = kv && is_edge((t0 + j) * BN) ? b_raw + st : b_full + st;
             if (h >= NS) wait(b_free + st, (h / NS - 1) & 1);
-            if (__all_sync(kFull, good)) {
-              if (lane == 0) mbar_expect_tx(bar, __popc(boxes) * a.box * HD * 2);
+            if (!__all_sync(kFull, good)) continue;
+            if (me == 0 && elect_one()) mbar_expect_tx(bar, __popc(boxes) * a.box * HD * 2);
+            for (int i = me; i < per_tile * NP; i += 3) {
+              const int c = i / NP, p = i % NP, pc = __shfl_sync(kFull, pg, c), oc = __shfl_sync(kFull, of, c);
+              if ((boxes >> c & 1) && elect_one())
+                tma_load_4d(sm + C::kQ + st * C::kStage + p * (BN * 128) + c * a.box * 128, kv ? &a.vmap : &a.kmap, p * 64,
+                            oc, a.pg.per_head ? 0 : w.kvh, pc, bar);
               __syncwarp();
-              for (int i0 = 0; i0 < per_tile * NP; i0 += 32) {
-                const int i = i0 + lane, c = (i / NP) & 31, p = i % NP;
-                const int pg = __shfl_sync(kFull, pid, c), of = __shfl_sync(kFull, off, c);
-                if (i < per_tile * NP && (boxes >> c & 1))
-                  tma_load_4d(sm + C::kQ + st * C::kStage + p * (BN * 128) + c * a.box * 128, (h & 1) ? &a.vmap : &a.kmap,
-                              p * 64, of, a.pg.per_head ? 0 : w.kvh, pg, bar);
-              }
             }
-            if ((h & 1) && h + 1 < 2 * n_tiles) look(t0 + (h >> 1) + 1);
           }
-        } else {
-          // edge tiles of V: zero what is not finite, and the rows of tokens that no row here sees
-          uint32_t seen = 0;  // parity of each stage's b_raw
-          for (int j = 0; j < n_tiles; ++j) {
-            if (!is_edge((t0 + j) * BN)) continue;
-            const int st = (2 * j + 1) % NS;
-            wait(b_raw + st, (seen >> st) & 1);
-            seen ^= 1u << st;
-            bool dirty = false;
-            if (good)
-              for (int i = lt - 32; i < BN * QC; i += 64) {
-                const uint32_t at = s_ring + st * C::kStage + i * 16;
-                const int tk = (t0 + j) * BN + i / 8 % BN;
-                uint4 x = lds128(at);
-                if (tk < lo || tk >= hi) sts128(at, make_uint4(0, 0, 0, 0));
-                else if (scrub<T>(x)) sts128(at, x), dirty = true;
-              }
-            if (dirty) ctl[1] = 1;
-            fence_async_smem();
-            named_sync<64>();
-            if (lt == 32) mbar_arrive(b_full + st);
-          }
+          if (j > 0) mend(j - 1);  // a tile late: the next one's boxes are on their way
         }
+        mend(n_tiles - 1);
       } else {
         // record offsets of a tile's tokens: table entries are loaded a tile ahead of their use
         constexpr int PT = (BN + kLoaders - 1) / kLoaders;
@@ -524,8 +547,7 @@ __global__ void __launch_bounds__(Config<MODE, HD>::kThreads, 1) kv_prefill_kern
         uint32_t v_par = 0, k_par = 0;
         for (int j = 0; j < n_tiles; ++j) {
           if (!warp_wait(b_full + sv, v_par)) break;
-          if (j + 1 < n_tiles && !warp_wait(b_full + sk, k_par)) break;
-          bool ok = true;
+          bool ok = true, have_k = false;
 #pragma unroll
           for (int t = 0; t < NQ; ++t) {
             if (j >= cnt[t]) continue;
@@ -533,8 +555,13 @@ __global__ void __launch_bounds__(Config<MODE, HD>::kThreads, 1) kv_prefill_kern
             pv(t, sv, 0, j > 0);
             if (!(ok = warp_wait(b_p + 2 * t + 1, j & 1))) break;
             pv(t, sv, 1, true);
-            if (j + 1 < cnt[t]) qk(t, sk);
-            else commit(b_o + t);
+            if (j + 1 < cnt[t]) {
+              if (!have_k && !(ok = warp_wait(b_full + sk, k_par))) break;
+              have_k = true;
+              qk(t, sk);
+            } else {
+              commit(b_o + t);
+            }
           }
           if (!ok) break;
           commit(b_free + sv);
@@ -549,24 +576,18 @@ __global__ void __launch_bounds__(Config<MODE, HD>::kThreads, 1) kv_prefill_kern
     }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kMore));
-    if (n_tiles > 0) {  // Q, while the loaders start
-      for (int i = tid; i < ROWS * QC; i += 256) {
-        const int rr = i / QC, ch = i % QC, row = w.first + rr, tk = row / a.G, h = row - tk * a.G;
-        const bool ok = row < end_row;
-        const char* src = a.q + (ok ? (w.q0 + tk) * a.q_b + ((int64_t)w.kvh * a.G + h) * (HD * 2) : 0) + ch * 16;
-        cp_async16(s_q + (rr >> 7) * (128 * HD * 2) + chunk_at<128>(rr & 127, ch), src, ok);
-      }
-      cp_commit();
+    if (n_tiles > 0) {
       cp_wait<0>();
       fence_async_smem();
       mbar_arrive(b_q);
+      asm volatile("bar.sync 2, 256;" ::: "memory");  // the epilogue writes where others' copies land
     }
     if (warp < 4 * NQ) {
     // ---- softmax ------------------------------------------------------------------------
     const int t = warp >> 2, i = w.first + t * 128 + (warp & 3) * 32 + lane;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t ts = tmem + t * C::kS + lanes, to = tmem + C::kO + t * HD + lanes;
-    const int tok = i / a.G, pos = p0 + tok;
+    const int tok = token_of(a, i), pos = p0 + tok;
     const int n = t == 0 ? cnt[0] : cnt[1], fmin = t == 0 ? tmin[0] : tmin[1], fmax = t == 0 ? tmax[0] : tmax[1];
     const float sl = a.scale_log2;
     float m = kNegHuge, l = 0.f;
@@ -636,6 +657,8 @@ __global__ void __launch_bounds__(Config<MODE, HD>::kThreads, 1) kv_prefill_kern
     const int64_t row = (w.q0 + tok) * a.hq + (int64_t)w.kvh * a.G + (i - tok * a.G);
     const bool fix = n > 0 && ctl[1] != 0;
     const float inv = l == 0.f ? 0.f : 1.f / l;  // no token (or no finite logit): zeros
+    // the rows' place in the Q tile, whose last product is done: they leave through it as whole lines
+    const uint32_t s_out = s_q + (t * 128 + (warp & 3) * 32) * (HD * 2);
     if (good) {
       float* part = a.splits > 1 ? a.part + ((int64_t)blockIdx.y * a.total_q * a.hq + row) * (HD + 4) : nullptr;
 #pragma unroll 1
@@ -696,15 +719,28 @@ __global__ void __launch_bounds__(Config<MODE, HD>::kThreads, 1) kv_prefill_kern
           for (int e = 0; e < 32; e += 4)
             *reinterpret_cast<uint4*>(part + c + e) = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
         } else {
-          uint4* dst = reinterpret_cast<uint4*>(a.out + (row * HD + c) * 2);
 #pragma unroll
           for (int e = 0; e < 32; e += 8) {
             float x[8];
 #pragma unroll
             for (int u = 0; u < 8; ++u) x[u] = __uint_as_float(o[e + u]) * inv;
-            dst[e / 8] = make_uint4(Half2<T>::pack(x[0], x[1]), Half2<T>::pack(x[2], x[3]), Half2<T>::pack(x[4], x[5]),
-                                    Half2<T>::pack(x[6], x[7]));
+            sts128(s_out + lane * (HD * 2) + (((c + e) / 8 ^ (lane & 7)) * 16),
+                   make_uint4(Half2<T>::pack(x[0], x[1]), Half2<T>::pack(x[2], x[3]), Half2<T>::pack(x[4], x[5]),
+                              Half2<T>::pack(x[6], x[7])));
           }
+        }
+      }
+      if (!part) {  // whole rows, 16 bytes a lane
+        __syncwarp();
+        const int row0 = i - lane;
+#pragma unroll 4
+        for (int x = lane; x < 32 * QC; x += 32) {
+          const int r = x / QC, ch = x % QC, ir = row0 + r;
+          if (ir >= end_row) break;
+          const int tk = token_of(a, ir);
+          const int64_t to_row = (w.q0 + tk) * a.hq + (int64_t)w.kvh * a.G + (ir - tk * a.G);
+          *reinterpret_cast<uint4*>(a.out + (to_row * HD + ch * 8) * 2) =
+              lds128(s_out + r * (HD * 2) + ((ch ^ (r & 7)) * 16));
         }
       }
       if (mine) {
@@ -728,7 +764,7 @@ __global__ void __launch_bounds__(256) kv_prefill_combine_kernel(const __grid_co
   const int lane = threadIdx.x & 31;
   const int64_t stride = a.total_q * a.hq * (HD + 4);
   for (int i = w.first + (threadIdx.x >> 5); i < w.first + ROWS && i < w.rows; i += 8) {
-    const int tok = i / a.G;
+    const int tok = token_of(a, i);
     const int64_t row = (w.q0 + tok) * a.hq + (int64_t)w.kvh * a.G + (i - tok * a.G);
     const float* p = a.part + row * (HD + 4);
     float m = kNegHuge, l = 0.f, o[E];
@@ -849,6 +885,9 @@ cudaError_t launch_kv_prefill(const tq_ctx* ctx, const PageView& pg, int format,
   a.pg = pg;
   a.q = static_cast<const char*>(q), a.q_b = q_stride * 2, a.total_q = total_q;
   a.batch = batch, a.hq = hq, a.G = hq / pg.hkv;
+  while ((1 << a.g_shift) < a.G) ++a.g_shift;
+  a.g_shift += 30;
+  a.g_mul = (uint32_t)((((uint64_t)1 << a.g_shift) + a.G - 1) / a.G);
   a.cu_q = cu_q, a.max_q = max_q, a.table = table, a.max_pages = max_pages, a.lens = seq_lens;
   a.max_len = max_len, a.window = window, a.scale_log2 = scale * 1.4426950408889634f;
   a.out = static_cast<char*>(out), a.lse = lse, a.err = ctx->d_err;

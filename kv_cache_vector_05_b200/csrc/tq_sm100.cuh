@@ -46,6 +46,23 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, uint32
   return false;
 }
 
+// The same with the hardware's own (short) suspension per poll: for handovers on a critical
+// path between warps that have nothing else to do.
+__device__ __forceinline__ bool mbar_spin(uint64_t* bar, uint32_t parity, unsigned long long ns = 2000000000ull) {
+  const uint32_t a = smem_u32(bar);
+  unsigned long long start = 0;
+  for (uint32_t it = 0;; ++it) {
+    uint32_t done;
+    asm volatile("{ .reg .pred p; mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2; selp.u32 %0, 1, 0, p; }"
+                 : "=r"(done)
+                 : "r"(a), "r"(parity)
+                 : "memory");
+    if (done) return true;
+    if (it == 0) start = global_ns();
+    else if ((it & 255) == 0 && global_ns() - start > ns) return false;
+  }
+}
+
 // Plain arrival on `bar` (release semantics at CTA scope).
 __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
