@@ -76,9 +76,11 @@ template <int MODE, int HD>
 struct Config {
   static constexpr bool MX = MODE == kMx;
   static constexpr int kThreads = MX ? 512 : 384, kLoaders = kThreads - 288;
-  // registers per thread: launched with kThreads * kLaunch, then moved to the softmax warps:
-  // 384: 256 * 216 + 128 * 72 = 384 * 168; 512: 256 * 168 + 256 * 88 = 512 * 128
-  static constexpr int kMore = MX ? 168 : 216, kLess = MX ? 88 : 72;
+  // 16-bit: registers move from the loaders to the softmax warps, 256 * 216 + 128 * 72 = 384 * 168,
+  // so that a row's whole S tile is held in them; MXFP4: its loaders need them too (128 each),
+  // and the softmax reads S in two halves, once for the maximum and once for the exponentials
+  static constexpr int kMore = 216, kLess = 72;
+  static constexpr int kCols = MX && HD < 256 ? 64 : (HD == 256 ? 64 : 128);  // columns of S held at once
   static constexpr int NQ = HD == 256 ? 1 : 2;    // row tiles
   static constexpr int BN = HD == 256 ? 64 : 128; // tokens per K / V tile
   static constexpr int kStage = BN * HD * 2;
@@ -155,6 +157,32 @@ __device__ __forceinline__ bool scrub(uint4& x) {
 __device__ __forceinline__ int token_of(const PreArgs& a, int row) {
   return (int)((uint64_t)(uint32_t)row * a.g_mul >> a.g_shift);
 }
+
+// A block of 32 MXFP4 codes as bf16 values code 2^(e - 32), exact for e >= -100. Register i of a
+// word's four holds coordinates (i, i + 4), whose nibbles lie at the same place of the word's
+// halves: the sign moves to bit 15 and the magnitude to bits 8-6 (there it reads code 2^-126, a
+// subnormal, as the product takes it), left shifts as integer products, because shifts and logic
+// share one half-rate pipe; then one multiplication by 2^(94 + e). WIDE: e > 33 or NaN, in two.
+// Q's coordinates are stored in the same order, O's columns are put back by name, and the
+// factors 2^-32 go into the logit scale and the final one.
+template <bool WIDE>
+__device__ __forceinline__ void mx_block(const uint32_t (&w)[4], uint32_t scale, uint32_t (&v)[16]) {
+  const uint32_t f = WIDE ? e8m0_bf16(scale) * 0x10001u : (scale + 94) * 0x800080u, two94 = 0x6e806e80u;
+  const __nv_bfloat162 f2 = *reinterpret_cast<const __nv_bfloat162*>(&f);
+  const __nv_bfloat162 k2 = *reinterpret_cast<const __nv_bfloat162*>(&two94);
+#pragma unroll
+  for (int c = 0; c < 4; ++c)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t y = i < 2 ? w[c] : w[c] >> 8, n = i & 1;
+      const uint32_t z = ((y * (n ? 256u : 4096u)) & 0x80008000u) | ((y * (n ? 4u : 64u)) & 0x01c001c0u);
+      __nv_bfloat162 u = *reinterpret_cast<const __nv_bfloat162*>(&z);
+      if constexpr (WIDE) u = __hmul2(u, k2);
+      u = __hmul2(u, f2);
+      v[4 * c + i] = *reinterpret_cast<const uint32_t*>(&u);
+    }
+}
+constexpr float kMxUp = 4294967296.f;  // 2^32
 
 // What a block works on.
 struct Block {
@@ -238,7 +266,14 @@ __global__ void __launch_bounds__(Config<MODE, HD>::kThreads, 1) kv_prefill_kern
       const int row = w.first + rr, tk = token_of(a, row), h = row - tk * a.G;
       const bool ok = row < end_row;
       const char* src = a.q + (ok ? (w.q0 + tk) * a.q_b + ((int64_t)w.kvh * a.G + h) * (HD * 2) : 0) + ch * 16;
-      cp_async16(s_q + (rr >> 7) * (128 * HD * 2) + chunk_at<128>(rr & 127, ch), src, ok);
+      const uint32_t dst = s_q + (rr >> 7) * (128 * HD * 2) + chunk_at<128>(rr & 127, ch);
+      if constexpr (MX) {  // coordinates in mx_block's order
+        const uint4 x = ok ? __ldg(reinterpret_cast<const uint4*>(src)) : make_uint4(0, 0, 0, 0);
+        sts128(dst, make_uint4(__byte_perm(x.x, x.z, 0x5410), __byte_perm(x.x, x.z, 0x7632),
+                               __byte_perm(x.y, x.w, 0x5410), __byte_perm(x.y, x.w, 0x7632)));
+      } else {
+        cp_async16(dst, src, ok);
+      }
     }
     cp_commit();
   }
@@ -287,7 +322,7 @@ __global__ void __launch_bounds__(Config<MODE, HD>::kThreads, 1) kv_prefill_kern
   };
 
   if (warp >= 8) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kLess));
+    if constexpr (!MX) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kLess));
     if (warp >= 9 && n_tiles > 0) {
       // ---- loaders --------------------------------------------------------------------
       const int lt = tid - 288;
@@ -437,32 +472,25 @@ __global__ void __launch_bounds__(Config<MODE, HD>::kThreads, 1) kv_prefill_kern
           constexpr int CPR = HD / 32, HALF = BN * CPR, NC = (2 * HALF + kLoaders - 1) / kLoaders;
           uint4 code[NC];
           uint32_t sc[NC];
-          auto fetch = [&](int kv0) {
-#pragma unroll
-            for (int i = 0; i < NC; ++i) {
-              const int x = lt + i * kLoaders, y = x >= HALF ? x - HALF : x, r = y / CPR, blk = y % CPR;
-              code[i] = make_uint4(0, 0, 0, 0);
-              sc[i] = 127;
-              if (x < 2 * HALF && kv0 + r >= lo && kv0 + r < hi) {
-                code[i] = __ldg(reinterpret_cast<const uint4*>((x < HALF ? a.pg.k : a.pg.v) + offs[r] + blk * 16));
-                sc[i] = __ldg((x < HALF ? a.pg.ks : a.pg.vs) + soffs[r] + blk);
-              }
+          auto fetch = [&](int i, int kv0) {
+            const int x = lt + i * kLoaders, y = x >= HALF ? x - HALF : x, r = y / CPR, blk = y % CPR;
+            code[i] = make_uint4(0, 0, 0, 0);
+            sc[i] = 127;
+            if (x < 2 * HALF && kv0 + r >= lo && kv0 + r < hi) {
+              code[i] = __ldg(reinterpret_cast<const uint4*>((x < HALF ? a.pg.k : a.pg.v) + offs[r] + blk * 16));
+              sc[i] = __ldg((x < HALF ? a.pg.ks : a.pg.vs) + soffs[r] + blk);
             }
           };
-          fetch(t0 * BN);
+#pragma unroll
+          for (int i = 0; i < NC; ++i) fetch(i, t0 * BN);
           if (n_tiles > 1) look(t0 + 1);
           for (int j = 0; j < n_tiles; ++j) {
             const int sk = (2 * j) % NS, sv = (2 * j + 1) % NS, kv0 = (t0 + j) * BN;
             const bool edge = is_edge(kv0);
-            uint4 cur[NC];
-            uint32_t cs[NC];
-#pragma unroll
-            for (int i = 0; i < NC; ++i) cur[i] = code[i], cs[i] = sc[i];
             if (j + 1 < n_tiles) {
               named_sync<kLoaders>();  // the offsets have been used
               place();
               named_sync<kLoaders>();
-              fetch(kv0 + BN);
               if (j + 2 < n_tiles) look(t0 + j + 2);
             }
             if (2 * j >= NS) wait(b_free + sk, (2 * j / NS - 1) & 1);
@@ -470,25 +498,17 @@ __global__ void __launch_bounds__(Config<MODE, HD>::kThreads, 1) kv_prefill_kern
 #pragma unroll
             for (int i = 0; i < NC; ++i) {
               const int x = lt + i * kLoaders, y = x >= HALF ? x - HALF : x, r = y / CPR, blk = y % CPR;
-              if (x >= 2 * HALF || !good) break;
               const uint32_t base = s_ring + (x < HALF ? sk : sv) * C::kStage;
-              const uint32_t wd[4] = {cur[i].x, cur[i].y, cur[i].z, cur[i].w};
-              const uint32_t f = e8m0_bf16(cs[i]) * 0x10001u, two112 = 0x77807780u;
-              const __nv_bfloat162 f2 = *reinterpret_cast<const __nv_bfloat162*>(&f);
-              const __nv_bfloat162 k2 = *reinterpret_cast<const __nv_bfloat162*>(&two112);
+              const uint32_t wd[4] = {code[i].x, code[i].y, code[i].z, code[i].w};
+              uint32_t v[16];
+              if (__any_sync(kFull, sc[i] > 160)) mx_block<true>(wd, sc[i], v);
+              else mx_block<false>(wd, sc[i], v);
+              if (j + 1 < n_tiles) fetch(i, kv0 + BN);
 #pragma unroll
               for (int c = 0; c < 4; ++c) {
-                uint32_t v[4];
-                e2m1x8_f16(wd[c], v);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                  const uint32_t z = (v[e] & 0x80008000u) | ((v[e] >> 3) & 0x0fff0fffu);  // code 2^-112 as bf16
-                  const __nv_bfloat162 u = __hmul2(__hmul2(*reinterpret_cast<const __nv_bfloat162*>(&z), k2), f2);
-                  v[e] = *reinterpret_cast<const uint32_t*>(&u);
-                }
-                uint4 o = make_uint4(v[0], v[1], v[2], v[3]);
+                uint4 o = make_uint4(v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
                 if (edge && x >= HALF && scrub<T>(o)) dirty = true;
-                sts128(base + chunk_at<BN>(r, blk * 4 + c), o);
+                if (x < 2 * HALF && good) sts128(base + chunk_at<BN>(r, blk * 4 + c), o);
               }
             }
             if (dirty) ctl[1] = 1;
@@ -575,7 +595,7 @@ __global__ void __launch_bounds__(Config<MODE, HD>::kThreads, 1) kv_prefill_kern
       }
     }
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kMore));
+    if constexpr (!MX) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kMore));
     if (n_tiles > 0) {
       cp_wait<0>();
       fence_async_smem();
@@ -589,29 +609,42 @@ __global__ void __launch_bounds__(Config<MODE, HD>::kThreads, 1) kv_prefill_kern
     const uint32_t ts = tmem + t * C::kS + lanes, to = tmem + C::kO + t * HD + lanes;
     const int tok = token_of(a, i), pos = p0 + tok;
     const int n = t == 0 ? cnt[0] : cnt[1], fmin = t == 0 ? tmin[0] : tmin[1], fmax = t == 0 ? tmax[0] : tmax[1];
-    const float sl = a.scale_log2;
+    const float sl = MX ? a.scale_log2 * kMxUp : a.scale_log2;
     float m = kNegHuge, l = 0.f;
     for (int j = 0; j < n; ++j) {
       if (!__all_sync(kFull, wait(b_s + t, j & 1))) break;
       fence_after_sync();
-      uint32_t s[BN];
-#pragma unroll
-      for (int c = 0; c < BN; c += 32) tmem_ld32(ts + c, *reinterpret_cast<uint32_t(*)[32]>(s + c));
-      tmem_ld_wait();
+      constexpr int NC = C::kCols;
+      uint32_t s[NC];
       const int kv0 = (t0 + j) * BN;
-      if (kv0 + BN - 1 > fmin || (wnd && kv0 <= fmax - wnd)) {
-        const int last = pos - kv0, from = wnd ? last - wnd + 1 : -1;  // columns seen: [from, last]
+      const bool edge = kv0 + BN - 1 > fmin || (wnd && kv0 <= fmax - wnd);
+      auto load = [&](int c0) {
 #pragma unroll
-        for (int c = 0; c < BN; ++c)
-          if (c > last || c < from) s[c] = 0xff800000u;
-      }
-      float mx = max3(s[0], s[1], s[2]), my = max3(s[3], s[4], s[5]);
+        for (int c = 0; c < NC; c += 32) tmem_ld32(ts + c0 + c, *reinterpret_cast<uint32_t(*)[32]>(s + c));
+        tmem_ld_wait();
+        if (edge) {
+          const int last = pos - kv0 - c0, from = wnd ? last - wnd + 1 : -1;  // columns seen: [from, last]
 #pragma unroll
-      for (int c = 6; c + 3 < BN; c += 4) {
-        mx = max3(__float_as_uint(mx), s[c], s[c + 1]);
-        my = max3(__float_as_uint(my), s[c + 2], s[c + 3]);
+          for (int c = 0; c < NC; ++c)
+            if (c > last || c < from) s[c] = 0xff800000u;
+        }
+      };
+      float mx = -INFINITY;
+#pragma unroll
+      for (int c0 = 0; c0 < BN; c0 += NC) {
+        load(c0);
+        float my = max3(s[0], s[1], s[2]);
+        mx = max3(__float_as_uint(mx), s[3], s[4]);
+#pragma unroll
+        for (int c = 5; c + 3 < NC; c += 4) {
+          mx = max3(__float_as_uint(mx), s[c], s[c + 1]);
+          my = max3(__float_as_uint(my), s[c + 2], s[c + 3]);
+        }
+        static_assert((NC - 5) % 4 == 3, "three columns are left");
+        mx = max3(__float_as_uint(mx), s[NC - 3], s[NC - 2]);
+        mx = max3(__float_as_uint(mx), __float_as_uint(my), s[NC - 1]);
       }
-      mx = max3(__float_as_uint(fmaxf(mx, my)), s[BN - 2], s[BN - 1]) * sl;
+      mx *= sl;
       const bool grown = mx > m + (kOff + kSlack);
       if (__any_sync(kFull, grown)) {  // rows that need none keep their m: f = 1
         const float mn = grown ? mx - kOff : m, f = ex2(m - mn);
@@ -634,9 +667,11 @@ __global__ void __launch_bounds__(Config<MODE, HD>::kThreads, 1) kv_prefill_kern
 #pragma unroll
       for (int c = 0; c < BN; c += 32) {
         uint32_t pk[16];
+        if (NC < BN && c % NC == 0) load(c);
 #pragma unroll
         for (int e = 0; e < 32; e += 2) {
-          const float2 x = fma2(make_float2(__uint_as_float(s[c + e]), __uint_as_float(s[c + e + 1])), sl2, nm2);
+          const int i = c % NC + e;
+          const float2 x = fma2(make_float2(__uint_as_float(s[i]), __uint_as_float(s[i + 1])), sl2, nm2);
           const float2 p = make_float2(ex2(x.x), ex2(x.y));
           sum = add2(sum, p);
           pk[e / 2] = Half2<T>::pack(p.x, p.y);
@@ -671,6 +706,13 @@ __global__ void __launch_bounds__(Config<MODE, HD>::kThreads, 1) kv_prefill_kern
         } else {
 #pragma unroll
           for (int e = 0; e < 32; ++e) o[e] = 0;
+        }
+        if constexpr (MX) {
+          uint32_t x[32];
+#pragma unroll
+          for (int e = 0; e < 32; ++e) x[e] = o[(e & ~7) + ((e & 3) * 2 + ((e >> 2) & 1))];
+#pragma unroll
+          for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(x[e]) * kMxUp);
         }
         if (!mine) continue;
         if (fix) {
