@@ -521,7 +521,8 @@ class KVPages:
         self.hkv = None if self.per_head else k.shape[2]
         self.n_pages, self.page_size = k.shape[0], k.shape[1]
         self.dtype = torch.bfloat16 if mx else k.dtype        # of q, of appended and of read rows
-        self.device = k.device
+        self.device, self.index = k.device, k.get_device()
+        self.code = _dtype_code(self.dtype)
         p = tq_kv_pages()
         p.format, p.pages_per_head = self.format, int(self.per_head)
         p.page_size, p.n_pages = self.page_size, self.n_pages
@@ -536,7 +537,7 @@ class KVPages:
 
     def struct(self, ctx: Context, hkv: int):
         """The C structure for `hkv` KV heads, checked against the context."""
-        if self.d != ctx.d or self.device.index != ctx.device:
+        if self.d != ctx.d or self.index != ctx.device:
             raise ValueError("the page cache has another d or device than the context")
         if not self.per_head and hkv != self.hkv:
             raise ValueError(f"the page cache holds {self.hkv} KV heads, not {hkv}")
@@ -548,18 +549,33 @@ class KVPages:
         return ctypes.byref(p)
 
 
+# The page calls serve decode steps whose kernels take a few microseconds, so their marshalling
+# looks at each tensor once and passes plain integers.
+
 def _rows(t, what: str, n: int, d: int, pages: KVPages) -> int:
     """Row stride of [n, heads, d] rows of the cache's 16-bit type with contiguous heads."""
-    if t.dim() != 3 or t.shape[0] != n or t.shape[2] != d or t.dtype != pages.dtype or t.device != pages.device:
+    shape = t.shape
+    if len(shape) != 3 or shape[0] != n or shape[2] != d or t.dtype is not pages.dtype or t.get_device() != pages.index:
         raise ValueError(f"{what} must be [{n}, heads, {d}] of {pages.dtype} on {pages.device}")
-    if t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != d):
+    s0, s1, s2 = t.stride()
+    if s2 != 1 or (s1 != d and shape[1] > 1):
         raise ValueError(f"{what} must have contiguous heads")
-    return t.stride(0) if n > 1 else t.shape[1] * d
+    return s0 if n > 1 else shape[1] * d
 
 
-def _index(t, what: str, dtype, shape, pages: KVPages):
-    if t.dtype != dtype or tuple(t.shape) != shape or not t.is_contiguous() or t.device != pages.device:
-        raise ValueError(f"{what} must be a contiguous {dtype} tensor of shape {shape} on {pages.device}")
+def _index(t, what: str, dtype, shape, pages: KVPages) -> int:
+    """Address of a contiguous tensor of this type and shape."""
+    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous() or t.get_device() != pages.index:
+        raise ValueError(f"{what} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {pages.device}")
+    return t.data_ptr()
+
+
+def _raw_stream(stream, index: int) -> int:
+    """cudaStream_t of `stream`, or of the current stream of device `index`."""
+    if stream is not None:
+        return stream.cuda_stream
+    import torch
+    return torch._C._cuda_getCurrentRawStream(index)
 
 
 def tq_append_kv_pages(ctx: Context, pages: KVPages, k, v, slot, q=None, q_out=None, cos_sin=None, positions=None,
@@ -569,33 +585,34 @@ def tq_append_kv_pages(ctx: Context, pages: KVPages, k, v, slot, q=None, q_out=N
     [n_positions, rot_dim]) at `positions` (int64 [n]) if given; q [n, hq, d] is rotated into
     q_out (a new tensor if None; may be q). Rows may be strided. Returns q_out."""
     import torch
-    n, hkv = k.shape[0], k.shape[1]
+    n, hkv, _ = k.shape
     p = pages.struct(ctx, hkv)
-    ks, vs = _rows(k, "k", n, ctx.d, pages), _rows(v, "v", n, ctx.d, pages)
+    d = ctx.d
+    ks, vs = _rows(k, "k", n, d, pages), _rows(v, "v", n, d, pages)
     if v.shape != k.shape:
         raise ValueError("k and v must have one shape")
-    _index(slot, "slot", torch.int64, (n, hkv) if pages.per_head else (n,), pages)
+    at = _index(slot, "slot", torch.int64, (n, hkv) if pages.per_head else (n,), pages)
     hq = qs = qos = 0
+    qp = qop = rope = None
     if q is not None:
-        hq, qs = q.shape[1], _rows(q, "q", n, ctx.d, pages)
+        hq, qs, qp = q.shape[1], _rows(q, "q", n, d, pages), q.data_ptr()
         if q_out is None:
-            q_out = torch.empty((n, hq, ctx.d), dtype=q.dtype, device=q.device)
-        qos = _rows(q_out, "q_out", n, ctx.d, pages)
+            q_out = torch.empty((n, hq, d), dtype=q.dtype, device=q.device)
+        qos, qop = _rows(q_out, "q_out", n, d, pages), q_out.data_ptr()
         if q_out.shape != q.shape:
             raise ValueError("q and q_out must have one shape")
     elif q_out is not None:
         raise ValueError("q_out without q")
-    rope = None
     if cos_sin is not None:
-        _index(positions, "positions", torch.int64, (n,), pages)
         if cos_sin.dim() != 2:
             raise ValueError("cos_sin must be [n_positions, rot_dim]")
-        _index(cos_sin, "cos_sin", torch.float32, tuple(cos_sin.shape), pages)
-        rope = ctypes.byref(tq_rope(cos_sin.data_ptr(), positions.data_ptr(), cos_sin.shape[0], cos_sin.shape[1],
-                                    int(interleaved)))
-    _check(lib.tq_append_kv_pages(ctx.handle, p, TQ_F16 if pages.dtype == torch.float16 else TQ_BF16, n, hq, _ptr(q),
-                                  qs, _ptr(k), ks, _ptr(v), vs, rope, _ptr(slot), _ptr(q_out), qos,
-                                  _stream(stream)), "tq_append_kv_pages")
+        rope = ctypes.byref(tq_rope(_index(cos_sin, "cos_sin", torch.float32, cos_sin.shape, pages),
+                                    _index(positions, "positions", torch.int64, (n,), pages), cos_sin.shape[0],
+                                    cos_sin.shape[1], interleaved))
+    status = lib.tq_append_kv_pages(ctx.handle, p, pages.code, n, hq, qp, qs, k.data_ptr(), ks, v.data_ptr(), vs, rope,
+                                    at, qop, qos, _raw_stream(stream, pages.index))
+    if status:
+        _check(status, "tq_append_kv_pages")
     return q_out
 
 
@@ -607,36 +624,47 @@ def tq_read_kv_pages(ctx: Context, pages: KVPages, slot, hkv: int, keys: bool = 
     import torch
     n = slot.shape[0]
     p = pages.struct(ctx, hkv)
-    _index(slot, "slot", torch.int64, (n, hkv) if pages.per_head else (n,), pages)
-    outs = []
+    at = _index(slot, "slot", torch.int64, (n, hkv) if pages.per_head else (n,), pages)
+    outs, ptrs = [], []
     for want, t, what in ((keys, k_out, "k_out"), (values, v_out, "v_out")):
-        if want and t is None:
+        if not want:
+            outs.append(None)
+            ptrs.append(None)
+            continue
+        if t is None:
             t = torch.empty((n, hkv, ctx.d), dtype=pages.dtype, device=pages.device)
-        elif want:
-            _index(t, what, pages.dtype, (n, hkv, ctx.d), pages)
-        outs.append(t if want else None)
-    _check(lib.tq_read_kv_pages(ctx.handle, p, n, _ptr(slot), _ptr(outs[0]), _ptr(outs[1]), _stream(stream)),
-           "tq_read_kv_pages")
+        outs.append(t)
+        ptrs.append(_index(t, what, pages.dtype, (n, hkv, ctx.d), pages))
+    status = lib.tq_read_kv_pages(ctx.handle, p, n, at, ptrs[0], ptrs[1], _raw_stream(stream, pages.index))
+    if status:
+        _check(status, "tq_read_kv_pages")
     return outs[0], outs[1]
 
 
 def _dtype_code(dtype) -> int:
     import torch
-    return {torch.float32: TQ_F32, torch.bfloat16: TQ_BF16, torch.float16: TQ_F16}[dtype]
+    if dtype is torch.float32:
+        return TQ_F32
+    if dtype is torch.bfloat16:
+        return TQ_BF16
+    if dtype is torch.float16:
+        return TQ_F16
+    raise ValueError(f"{dtype} is none of float32, bfloat16, float16")
 
 
-def _table(block_table, batch: int, hkv: int, pages: KVPages):
+def _table(block_table, batch: int, hkv: int, pages: KVPages) -> int:
     import torch
-    lead = (batch, hkv) if pages.per_head else (batch,)
-    _index(block_table, "block_table", torch.int32, lead + (block_table.shape[-1],), pages)
+    width = block_table.shape[-1]
+    return _index(block_table, "block_table", torch.int32, (batch, hkv, width) if pages.per_head else (batch, width),
+                  pages)
 
 
-def _workspace(workspace, need: int, device):
+def _workspace(workspace, need: int, pages: KVPages):
     import torch
     if workspace is None:
-        return torch.empty(max(need, 256), dtype=torch.uint8, device=device)
-    if workspace.device != device or not workspace.is_contiguous():
-        raise ValueError(f"the workspace must be a contiguous tensor on {device}")
+        return torch.empty(max(need, 256), dtype=torch.uint8, device=pages.device)
+    if workspace.get_device() != pages.index or not workspace.is_contiguous():
+        raise ValueError(f"the workspace must be a contiguous tensor on {pages.device}")
     return workspace
 
 
@@ -653,26 +681,24 @@ def tq_decode_kv_pages(ctx: Context, q, pages: KVPages, hkv: int, block_table, m
     [batch, hq, d] is fp32 or of q's type (`out_dtype`, default fp32, if it is allocated here).
     Returns (out, lse [batch, hq] fp32), to be merged with other token ranges by tq_merge_attention."""
     import torch
-    batch, hq = q.shape[0], q.shape[1]
+    batch, hq, d = q.shape
     p = pages.struct(ctx, hkv)
     qs = _rows(q, "q", batch, ctx.d, pages)
-    _table(block_table, batch, hkv, pages)
-    if seq_lens is not None:
-        _index(seq_lens, "seq_lens", torch.int32, (batch,), pages)
+    table = _table(block_table, batch, hkv, pages)
+    lens = None if seq_lens is None else _index(seq_lens, "seq_lens", torch.int32, (batch,), pages)
     if out is None:
-        out = torch.empty((batch, hq, ctx.d), dtype=out_dtype or torch.float32, device=q.device)
-    else:
-        _index(out, "out", out.dtype, (batch, hq, ctx.d), pages)
+        out = torch.empty((batch, hq, d), dtype=out_dtype or torch.float32, device=q.device)
     if lse is None:
         lse = torch.empty((batch, hq), dtype=torch.float32, device=q.device)
-    else:
-        _index(lse, "lse", torch.float32, (batch, hq), pages)
     need = lib.tq_decode_kv_pages_workspace_bytes(ctx.handle, batch, hq, hkv) if workspace is None else 0
-    workspace = _workspace(workspace, need, q.device)
-    _check(lib.tq_decode_kv_pages(
-        ctx.handle, p, _ptr(q), _dtype_code(q.dtype), qs, batch, hq, _ptr(block_table), block_table.shape[-1],
-        _ptr(seq_lens), max_len, window, softmax_scale, _ptr(out), _dtype_code(out.dtype), _ptr(lse),
-        _ptr(workspace), workspace.numel() * workspace.element_size(), _stream(stream)), "tq_decode_kv_pages")
+    workspace = _workspace(workspace, need, pages)
+    status = lib.tq_decode_kv_pages(
+        ctx.handle, p, q.data_ptr(), pages.code, qs, batch, hq, table, block_table.shape[-1], lens, max_len, window,
+        softmax_scale, _index(out, "out", out.dtype, q.shape, pages), _dtype_code(out.dtype),
+        _index(lse, "lse", torch.float32, (batch, hq), pages), workspace.data_ptr(), workspace.nbytes,
+        _raw_stream(stream, pages.index))
+    if status:
+        _check(status, "tq_decode_kv_pages")
     return out, lse
 
 
@@ -690,27 +716,25 @@ def tq_prefill_kv_pages(ctx: Context, q, pages: KVPages, hkv: int, block_table, 
     arguments as tq_decode_kv_pages. Returns (out of q's type, lse [total_q, hq] fp32); rows of no
     sequence keep what out and lse held."""
     import torch
-    total_q, hq, batch = q.shape[0], q.shape[1], cu_q.shape[0] - 1
+    (total_q, hq, d), batch = q.shape, cu_q.shape[0] - 1
     p = pages.struct(ctx, hkv)
     qs = _rows(q, "q", total_q, ctx.d, pages)
-    _index(cu_q, "cu_q", torch.int32, (batch + 1,), pages)
-    _table(block_table, batch, hkv, pages)
-    if seq_lens is not None:
-        _index(seq_lens, "seq_lens", torch.int32, (batch,), pages)
+    starts = _index(cu_q, "cu_q", torch.int32, (batch + 1,), pages)
+    table = _table(block_table, batch, hkv, pages)
+    lens = None if seq_lens is None else _index(seq_lens, "seq_lens", torch.int32, (batch,), pages)
     if out is None:
-        out = torch.empty((total_q, hq, ctx.d), dtype=q.dtype, device=q.device)
-    else:
-        _index(out, "out", q.dtype, (total_q, hq, ctx.d), pages)
+        out = torch.empty((total_q, hq, d), dtype=q.dtype, device=q.device)
     if lse is None:
         lse = torch.empty((total_q, hq), dtype=torch.float32, device=q.device)
-    else:
-        _index(lse, "lse", torch.float32, (total_q, hq), pages)
     need = 0
     if workspace is None:
         need = lib.tq_prefill_kv_pages_workspace_bytes(ctx.handle, total_q, batch, hq, hkv, max_len, max_q)
-    workspace = _workspace(workspace, need, q.device)
-    _check(lib.tq_prefill_kv_pages(
-        ctx.handle, p, _ptr(q), _dtype_code(q.dtype), qs, total_q, batch, hq, _ptr(cu_q), max_q, _ptr(block_table),
-        block_table.shape[-1], _ptr(seq_lens), max_len, window, softmax_scale, _ptr(out), _ptr(lse),
-        _ptr(workspace), workspace.numel() * workspace.element_size(), _stream(stream)), "tq_prefill_kv_pages")
+    workspace = _workspace(workspace, need, pages)
+    status = lib.tq_prefill_kv_pages(
+        ctx.handle, p, q.data_ptr(), pages.code, qs, total_q, batch, hq, starts, max_q, table, block_table.shape[-1],
+        lens, max_len, window, softmax_scale, _index(out, "out", q.dtype, q.shape, pages),
+        _index(lse, "lse", torch.float32, (total_q, hq), pages), workspace.data_ptr(), workspace.nbytes,
+        _raw_stream(stream, pages.index))
+    if status:
+        _check(status, "tq_prefill_kv_pages")
     return out, lse

@@ -35,6 +35,7 @@
 // finishes it (blocks of e > 15 or NaN take two multiplications). A key block of scale 2^-127,
 // the smallest, counts as zero.
 #include <algorithm>
+#include <atomic>
 
 #include "kv_pages.cuh"
 #include "tq_device.cuh"
@@ -867,11 +868,15 @@ __global__ void __launch_bounds__(256) kv_combine_kernel(const DecArgs a, int f1
 }
 
 template <typename T, int FMT, int HD, bool SMALL, bool WHOLE>
-cudaError_t run(const DecArgs& a, int ctas, cudaStream_t st) {
+cudaError_t run(const DecArgs& a, int device, int ctas, cudaStream_t st) {
   using C = Config<FMT, HD>;
   auto kern = kv_decode_kernel<T, FMT, HD, SMALL, WHOLE>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
-  if (e != cudaSuccess) return e;
+  static std::atomic<uint64_t> configured{0};  // devices on which the kernel may use its shared memory
+  cudaError_t e;
+  if (device >= 64 || !(configured.load() >> device & 1)) {
+    if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem)) != cudaSuccess) return e;
+    if (device < 64) configured.fetch_or((uint64_t)1 << device);
+  }
   kern<<<ctas, C::kWarps * 32, C::kSmem, st>>>(a);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
@@ -887,17 +892,17 @@ cudaError_t run(const DecArgs& a, int ctas, cudaStream_t st) {
 }
 
 template <typename T, int FMT, int HD>
-cudaError_t pick(const DecArgs& a, int ctas, cudaStream_t st) {
+cudaError_t pick(const DecArgs& a, int device, int ctas, cudaStream_t st) {
   const bool whole = a.pg.page_size % kTile == 0;
-  if (a.GB <= 4) return whole ? run<T, FMT, HD, true, true>(a, ctas, st) : run<T, FMT, HD, true, false>(a, ctas, st);
-  return whole ? run<T, FMT, HD, false, true>(a, ctas, st) : run<T, FMT, HD, false, false>(a, ctas, st);
+  if (a.GB <= 4) return whole ? run<T, FMT, HD, true, true>(a, device, ctas, st) : run<T, FMT, HD, true, false>(a, device, ctas, st);
+  return whole ? run<T, FMT, HD, false, true>(a, device, ctas, st) : run<T, FMT, HD, false, false>(a, device, ctas, st);
 }
 
 template <typename T, int FMT>
-cudaError_t pick_d(int d, const DecArgs& a, int ctas, cudaStream_t st) {
-  if (d == 64) return pick<T, FMT, 64>(a, ctas, st);
-  if (d == 128) return pick<T, FMT, 128>(a, ctas, st);
-  return pick<T, FMT, 256>(a, ctas, st);
+cudaError_t pick_d(int d, const DecArgs& a, int device, int ctas, cudaStream_t st) {
+  if (d == 64) return pick<T, FMT, 64>(a, device, ctas, st);
+  if (d == 128) return pick<T, FMT, 128>(a, device, ctas, st);
+  return pick<T, FMT, 256>(a, device, ctas, st);
 }
 
 constexpr int kMostWarps = 16;
@@ -929,9 +934,9 @@ cudaError_t launch_kv_decode(const tq_ctx* ctx, const PageView& pg, int format, 
   a.part = reinterpret_cast<float*>(a.meta + ctas);
   a.head = a.part + 2 * ctas * row;
   const int d = ctx->shape.d;
-  if (format == TQ_KV_MXFP4) return pick_d<__nv_bfloat16, TQ_KV_MXFP4>(d, a, ctas, stream);
-  if (format == TQ_KV_BF16) return pick_d<__nv_bfloat16, TQ_KV_BF16>(d, a, ctas, stream);
-  return pick_d<__half, TQ_KV_F16>(d, a, ctas, stream);
+  if (format == TQ_KV_MXFP4) return pick_d<__nv_bfloat16, TQ_KV_MXFP4>(d, a, ctx->device, ctas, stream);
+  if (format == TQ_KV_BF16) return pick_d<__nv_bfloat16, TQ_KV_BF16>(d, a, ctx->device, ctas, stream);
+  return pick_d<__half, TQ_KV_F16>(d, a, ctx->device, ctas, stream);
 }
 
 }  // namespace tq
