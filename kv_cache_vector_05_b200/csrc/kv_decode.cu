@@ -160,7 +160,7 @@ struct Cursor {
   int b, uk, tile;
   int blk;      // block-table index of the tile's first token
   int off;      // its place in the page (pages of whole tiles)
-  int64_t page; // page id, loaded ahead of its use
+  int page;     // its entry of the block table, loaded ahead of its use and checked then
 };
 
 template <typename T, int FMT, int HD, bool SMALL, bool WHOLE>
@@ -189,14 +189,14 @@ struct Worker {
 
   // ---- loads ------------------------------------------------------------------------
 
-  __device__ __forceinline__ int64_t page_of(const Cursor& u, int blk) const {
+  __device__ __forceinline__ int page_of(const Cursor& u, int blk) const {
     const int64_t row = a.pg.per_head ? (int64_t)u.b * a.pg.hkv + u.uk / a.HB : u.b;
-    int64_t p = __ldg(a.table + row * a.max_pages + blk);
-    if (p < 0 || p >= a.pg.n_pages) {
-      atomicOr(a.err, kErrIndex);
-      p = 0;
-    }
-    return p;
+    return __ldg(a.table + row * a.max_pages + blk);
+  }
+  __device__ __forceinline__ int64_t checked(int page) const {
+    if ((unsigned)page < (unsigned)a.pg.n_pages) return page;
+    atomicOr(a.err, kErrIndex);
+    return 0;
   }
 
   // Enter unit (b, uk) at `tile`; the page of the tile is looked up at once for WHOLE pages.
@@ -238,14 +238,15 @@ struct Worker {
     const int kvh = u.uk / a.HB;
     int64_t off0 = 0, soff0 = 0;
     if constexpr (WHOLE) {
-      off0 = u.page * a.pg.page_b + (int64_t)u.off * a.pg.tok_b + (int64_t)kvh * a.pg.head_b;
-      if constexpr (MX) soff0 = u.page * a.pg.spage_b + (int64_t)u.off * a.pg.stok_b + (int64_t)kvh * a.pg.shead_b;
+      const int64_t pg = checked(u.page);
+      off0 = pg * a.pg.page_b + (int64_t)u.off * a.pg.tok_b + (int64_t)kvh * a.pg.head_b;
+      if constexpr (MX) soff0 = pg * a.pg.spage_b + (int64_t)u.off * a.pg.stok_b + (int64_t)kvh * a.pg.shead_b;
     } else {
       // each of 16 lanes looks up one token's page; the others receive it by shuffles
       int tok = t + (lane & 15);
       tok = tok < u.e.lo ? u.e.lo : tok >= u.e.len ? u.e.len - 1 : tok;
       const int blk = tok / (int)a.pg.page_size, o = tok - blk * (int)a.pg.page_size;
-      const int64_t pg = page_of(u, blk);
+      const int64_t pg = checked(page_of(u, blk));
       off0 = pg * a.pg.page_b + (int64_t)o * a.pg.tok_b + (int64_t)kvh * a.pg.head_b;
       if constexpr (MX) soff0 = pg * a.pg.spage_b + (int64_t)o * a.pg.stok_b + (int64_t)kvh * a.pg.shead_b;
     }
@@ -602,6 +603,12 @@ __device__ __forceinline__ void store4(const DecArgs& a, bool f16, int64_t at, f
   }
 }
 
+// total * i / n, in 32 bits where they suffice.
+__device__ __forceinline__ int64_t scaled(int64_t total, int64_t i, int64_t n) {
+  const int64_t x = total * i;
+  return (total * n >> 32) == 0 ? (int64_t)((uint32_t)x / (uint32_t)n) : x / n;
+}
+
 __device__ __forceinline__ int64_t warp_incl_scan(int64_t v, int lane) {
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -625,56 +632,68 @@ __global__ void __launch_bounds__(Config<FMT, HD>::kWarps * 32, 1) kv_decode_ker
   const int upb = a.pg.hkv * a.HB;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
-  // sequences without tokens: zero rows
-  for (int b = blockIdx.x; b < a.batch; b += gridDim.x) {
-    if (extent(a, b).nt) continue;
-    for (int i = tid; i < a.hq * (HD / 4); i += NT)
-      store4(a, std::is_same<T, __half>::value, (int64_t)b * a.hq * HD + i * 4, make_float4(0.f, 0.f, 0.f, 0.f));
-    if (a.lse)
-      for (int h = tid; h < a.hq; h += NT) a.lse[(int64_t)b * a.hq + h] = -INFINITY;
-  }
-
   // all tiles, then the sequence in which this CTA's range starts
-  int64_t sum = 0;
-  for (int b = tid; b < a.batch; b += NT) sum += extent(a, b).nt;
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kFull, sum, o);
-  if (lane == 0) s_scan[w] = sum;
-  __syncthreads();
-  int64_t total = 0;
-#pragma unroll
-  for (int i = 0; i < W; ++i) total += s_scan[i];
-  total *= upb;
-  const int64_t want = (total + W * kMinTiles - 1) / (W * kMinTiles);
-  const int n = (int)(want < gridDim.x ? want : gridDim.x);
   const int k = blockIdx.x;
-  if (tid == 0) a.meta[k] = make_int4(0, 0, 0, 0);
-  if (k >= n) return;
-  const int64_t cta0 = total * k / n;
-  for (int64_t base = 0, b0 = 0;; b0 += NT) {
-    const int b = (int)b0 + tid;
-    const int64_t mine = b < a.batch ? (int64_t)extent(a, b).nt * upb : 0;
+  int64_t total, cta0;
+  int n;
+  auto divide = [&](int64_t all) {
+    total = all * upb;
+    const int64_t want = (total + W * kMinTiles - 1) / (W * kMinTiles);
+    n = (int)(want < gridDim.x ? want : gridDim.x);
+    cta0 = n ? scaled(total, k, n) : 0;
+  };
+  if (a.batch <= NT) {  // one scan gives both
+    const int64_t mine = tid < a.batch ? extent(a, tid).nt : 0;
     const int64_t incl = warp_incl_scan(mine, lane);
-    __syncthreads();  // s_scan has been read
     if (lane == 31) s_scan[w] = incl;
     __syncthreads();
-    int64_t before = base, all = base;
+    int64_t before = incl - mine, all = 0;
 #pragma unroll
     for (int i = 0; i < W; ++i) {
       if (i < w) before += s_scan[i];
       all += s_scan[i];
     }
-    if (mine && before + incl - mine <= cta0 && cta0 < before + incl) {
-      s_b = b;
-      s_start = before + incl - mine;
+    divide(all);
+    if (mine && k < n && before * upb <= cta0 && cta0 < (before + mine) * upb) {
+      s_b = tid;
+      s_start = before * upb;
     }
-    base = all;
-    if (cta0 < base) break;
+  } else {
+    int64_t sum = 0;
+    for (int b = tid; b < a.batch; b += NT) sum += extent(a, b).nt;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kFull, sum, o);
+    if (lane == 0) s_scan[w] = sum;
+    __syncthreads();
+    int64_t all = 0;
+#pragma unroll
+    for (int i = 0; i < W; ++i) all += s_scan[i];
+    divide(all);
+    int64_t base = 0;
+    for (int64_t b0 = 0; k < n && base <= cta0; b0 += NT) {
+      const int b = (int)b0 + tid;
+      const int64_t mine = b < a.batch ? (int64_t)extent(a, b).nt * upb : 0;
+      const int64_t incl = warp_incl_scan(mine, lane);
+      __syncthreads();  // s_scan has been read
+      if (lane == 31) s_scan[w] = incl;
+      __syncthreads();
+      int64_t before = base + incl - mine;
+#pragma unroll
+      for (int i = 0; i < W; ++i) {
+        if (i < w) before += s_scan[i];
+        base += s_scan[i];
+      }
+      if (mine && before <= cta0 && cta0 < before + mine) {
+        s_b = b;
+        s_start = before;
+      }
+    }
   }
+  if (tid == 0) a.meta[k] = make_int4(0, 0, 0, 0);
   __syncthreads();
 
   const int64_t nw = (int64_t)n * W, gw = (int64_t)k * W + w;
-  const int64_t r0 = total * gw / nw, r1 = total * (gw + 1) / nw;
+  const int64_t r0 = k < n ? scaled(total, gw, nw) : 0, r1 = k < n ? scaled(total, gw + 1, nw) : 0;
   if (lane < 2) s_pb[2 * w + lane] = -1;
   Worker<T, FMT, HD, SMALL, WHOLE> wk(a, smem_u32(smem) + w * C::kRing, lane);
   Cursor ld{}, cur{};
@@ -693,12 +712,15 @@ __global__ void __launch_bounds__(Config<FMT, HD>::kWarps * 32, 1) kv_decode_ker
     ld = cur;
     wk.place(ld);
     int64_t left = r1 - r0;  // tiles not yet issued
+    Cursor first[C::kStages - 1];  // their table entries are fetched together
 #pragma unroll
     for (int s = 0; s < C::kStages - 1; ++s) {
-      if (left > 0) {
-        wk.issue(ld, s);
-        if (--left) wk.advance(ld);
-      }
+      first[s] = ld;
+      if (left - s > 1) wk.advance(ld);
+    }
+#pragma unroll
+    for (int s = 0; s < C::kStages - 1; ++s) {
+      if (left > 0) wk.issue(first[s], s), --left;
       cp_commit();
     }
     seg_from = cur.tile;
@@ -761,41 +783,37 @@ __global__ void __launch_bounds__(Config<FMT, HD>::kWarps * 32, 1) kv_decode_ker
   }
   __syncthreads();
 
-  // merge runs of pieces of one unit, in token order
-  for (int i = 0; i < 2 * W;) {
-    if (s_pb[i] < 0) {
-      ++i;
-      continue;
-    }
-    int last = i;
-    for (int j = i + 1; j < 2 * W; ++j) {
-      if (s_pb[j] < 0) continue;
-      if (s_pb[j] != s_pb[i] || s_uk[j] != s_uk[i]) break;
-      last = j;
-    }
-    const int b = s_pb[i], uk = s_uk[i], kvh = uk / a.HB, hb = uk - kvh * a.HB;
+  // merge runs of pieces of one unit, in token order; lane i knows piece i
+  const int pb = lane < 2 * W ? s_pb[lane] : -1, puk = pb >= 0 ? s_uk[lane] : -1;
+  uint32_t todo = __ballot_sync(kFull, pb >= 0);
+  while (todo) {
+    const int i = __ffs(todo) - 1, b = __shfl_sync(kFull, pb, i), uk = __shfl_sync(kFull, puk, i);
+    const uint32_t run = todo & __ballot_sync(kFull, pb == b && puk == uk);
+    todo &= ~run;
+    const int last = 31 - __clz(run), kvh = uk / a.HB, hb = uk - kvh * a.HB;
     const int heads = min(a.GB, a.G - hb * a.GB);
     const bool whole = s_from[i] == 0 && s_to[last] == s_nt[i];
     const int64_t row0 = (int64_t)b * a.hq + kvh * a.G + hb * a.GB;
     float* part = a.part + (int64_t)(2 * k + (s_tile0[i] == cta0 ? 0 : 1)) * a.GB * kRow;
     for (int x = tid; x < heads * (HD / 4); x += NT) {
       const int h = x / (HD / 4), d0 = (x % (HD / 4)) * 4;
+      auto piece = [&](int j) {
+        return (j & 1 ? pieces + (j >> 1) * a.GB * kRow : a.head + ((int64_t)k * W + (j >> 1)) * a.GB * kRow) + h * kRow;
+      };
       float mx = kNegHuge;
-      for (int j = i; j <= last; ++j)
-        if (s_pb[j] >= 0) {
-          const float* pc = (j & 1 ? pieces + (j >> 1) * a.GB * kRow
-                                   : a.head + ((int64_t)k * W + (j >> 1)) * a.GB * kRow) + h * kRow;
-          mx = fmaxf(mx, pc[HD]);
-        }
+#pragma unroll
+      for (int j = 0; j < 2 * W; ++j)
+        if (run >> j & 1) mx = fmaxf(mx, piece(j)[HD]);
       float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
       float ls = 0.f;
-      for (int j = i; j <= last; ++j)
-        if (s_pb[j] >= 0) {
-          const float* pc = (j & 1 ? pieces + (j >> 1) * a.GB * kRow
-                                   : a.head + ((int64_t)k * W + (j >> 1)) * a.GB * kRow) + h * kRow;
-          const float f = ex2(pc[HD] - mx);
+#pragma unroll
+      for (int j = 0; j < 2 * W; ++j)
+        if (run >> j & 1) {
+          const float* pc = piece(j);
+          const float2 ml = *reinterpret_cast<const float2*>(pc + HD);
+          const float f = ex2(ml.x - mx);
           const float4 v = *reinterpret_cast<const float4*>(pc + d0);
-          ls = fmaf(f, pc[HD + 1], ls);
+          ls = fmaf(f, ml.y, ls);
           o.x = fmaf(f, v.x, o.x), o.y = fmaf(f, v.y, o.y), o.z = fmaf(f, v.z, o.z), o.w = fmaf(f, v.w, o.w);
         }
       if (whole) {
@@ -812,7 +830,15 @@ __global__ void __launch_bounds__(Config<FMT, HD>::kWarps * 32, 1) kv_decode_ker
       const int64_t end = s_tile0[i] + s_nt[i];
       a.meta[k] = make_int4(b, uk, (int)((end * n - 1) / total), 1 + (s_tile0[i] == cta0 ? 0 : 1));
     }
-    i = last + 1;
+  }
+
+  // sequences without tokens: zero rows
+  for (int b = k; b < a.batch; b += gridDim.x) {
+    if (extent(a, b).nt) continue;
+    for (int i = tid; i < a.hq * (HD / 4); i += NT)
+      store4(a, std::is_same<T, __half>::value, (int64_t)b * a.hq * HD + i * 4, make_float4(0.f, 0.f, 0.f, 0.f));
+    if (a.lse)
+      for (int h = tid; h < a.hq; h += NT) a.lse[(int64_t)b * a.hq + h] = -INFINITY;
   }
 }
 
@@ -834,16 +860,28 @@ __global__ void __launch_bounds__(256) kv_combine_kernel(const DecArgs a, int f1
     const int slot = i == 0 ? 2 * k0 + mt.w - 1 : 2 * (k0 + i);
     return a.part + ((int64_t)slot * a.GB + h) * kRow;
   };
+  // four partials in flight per group
   float m = kNegHuge, l = 0.f;
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int i = g; i < count; i += kGroups) m = fmaxf(m, row(i)[HD]);
-#pragma unroll 4
-  for (int i = g; i < count; i += kGroups) {
-    const float* p = row(i);
-    const float f = ex2(p[HD] - m);
-    const float4 v = *reinterpret_cast<const float4*>(p + 4 * x);
-    l = fmaf(f, p[HD + 1], l);
-    o.x = fmaf(f, v.x, o.x), o.y = fmaf(f, v.y, o.y), o.z = fmaf(f, v.z, o.z), o.w = fmaf(f, v.w, o.w);
+  for (int i = g; i < count; i += 4 * kGroups) {
+    float2 ml[4];
+    float4 v[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const bool ok = i + u * kGroups < count;
+      const float* p = row(ok ? i + u * kGroups : i);
+      ml[u] = *reinterpret_cast<const float2*>(p + HD);
+      v[u] = *reinterpret_cast<const float4*>(p + 4 * x);
+      if (!ok) ml[u] = make_float2(kNegHuge, 0.f), v[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    const float mn = fmaxf(m, fmaxf(fmaxf(ml[0].x, ml[1].x), fmaxf(ml[2].x, ml[3].x))), f0 = ex2(m - mn);
+    m = mn, l *= f0, o.x *= f0, o.y *= f0, o.z *= f0, o.w *= f0;
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const float f = ex2(ml[u].x - m);
+      l = fmaf(f, ml[u].y, l);
+      o.x = fmaf(f, v[u].x, o.x), o.y = fmaf(f, v[u].y, o.y), o.z = fmaf(f, v[u].z, o.z), o.w = fmaf(f, v[u].w, o.w);
+    }
   }
   s_o[g][x] = o;
   if (x == 0) s_m[g] = m, s_l[g] = l;
