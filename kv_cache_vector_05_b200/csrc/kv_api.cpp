@@ -82,6 +82,9 @@ tq_status view_pages(const char* fn, const tq_ctx* c, const tq_kv_pages* p, tq::
   w.spage_b = mx ? p->scale_page_stride : 0, w.stok_b = mx ? p->scale_token_stride : 0;
   w.shead_b = mx && !p->pages_per_head ? p->scale_head_stride : 0;
   w.page_size = p->page_size, w.n_pages = p->n_pages, w.n_slots = p->n_pages * p->page_size;
+  w.page_shift = -1;
+  if ((w.page_size & (w.page_size - 1)) == 0)
+    for (w.page_shift = 0; (int64_t(1) << w.page_shift) < w.page_size;) ++w.page_shift;
   w.hkv = p->hkv, w.per_head = p->pages_per_head;
   return TQ_OK;
 }

@@ -16,6 +16,7 @@
 
 #include "kv_pages.cuh"
 #include "tq_device.cuh"
+#include "tq_sm100.cuh"
 
 namespace tq {
 namespace {
@@ -41,111 +42,132 @@ struct AppendArgs {
 };
 
 constexpr int kThreads = 256;
-constexpr int kUnroll = 4;  // vectors in flight per lane: 8 16-byte loads
+constexpr int kUnroll = 2;      // vectors in flight per lane
+constexpr int kMostGroups = 8;  // most groups (see append_kernel) per warp
 
-// The rotated (or copied) chunk `ch` of one vector as fp32.
+// The 8 coordinates of a chunk as fp32.
 template <typename T>
-__device__ __forceinline__ void turn(const uint4& own, const uint4& par, int mode, const float (&c)[8],
-                                     const float (&s)[8], float (&y)[8]) {
-  const uint32_t w[4] = {own.x, own.y, own.z, own.w}, p[4] = {par.x, par.y, par.z, par.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float2 a = Half2<T>::unpack(w[i]);
-    y[2 * i] = a.x;
-    y[2 * i + 1] = a.y;
-  }
-  if (mode == 0) return;
-  if (mode == 3) {  // pairs (2i, 2i + 1) lie in the chunk; c, s hold their four angles
+__device__ __forceinline__ void unpack8(const uint4& x, float2 (&y)[4]) {
+  y[0] = Half2<T>::unpack(x.x), y[1] = Half2<T>::unpack(x.y);
+  y[2] = Half2<T>::unpack(x.z), y[3] = Half2<T>::unpack(x.w);
+}
+
+// Rotate a chunk in place. Halves: its own coordinates times cosines plus the pairs' others times
+// signed sines (-sin where the chunk holds the first coordinates: a c + b (-s) rounds like
+// a c - b s). Interleaved: the pairs lie in the chunk, c and s hold their four angles.
+template <typename T>
+__device__ __forceinline__ void turn(float2 (&y)[4], const uint4& par, bool interleaved, const float2 (&c)[4],
+                                     const float2 (&s)[4]) {
+  using namespace sm100;
+  if (interleaved) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const float a = y[2 * i], b = y[2 * i + 1];
-      y[2 * i] = __fsub_rn(__fmul_rn(a, c[i]), __fmul_rn(b, s[i]));
-      y[2 * i + 1] = __fadd_rn(__fmul_rn(b, c[i]), __fmul_rn(a, s[i]));
+      const float ci = i & 1 ? c[i / 2].y : c[i / 2].x, si = i & 1 ? s[i / 2].y : s[i / 2].x;
+      const float a = y[i].x, b = y[i].y;
+      y[i].x = __fsub_rn(__fmul_rn(a, ci), __fmul_rn(b, si));
+      y[i].y = __fadd_rn(__fmul_rn(b, ci), __fmul_rn(a, si));
     }
-    return;
-  }
-  // mode 1: this chunk holds the pairs' first coordinates, 2: the second ones
+  } else {
+    float2 z[4];
+    unpack8<T>(par, z);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float2 b = Half2<T>::unpack(p[i]);
-    const float b0 = __fmul_rn(b.x, s[2 * i]), b1 = __fmul_rn(b.y, s[2 * i + 1]);
-    const float a0 = __fmul_rn(y[2 * i], c[2 * i]), a1 = __fmul_rn(y[2 * i + 1], c[2 * i + 1]);
-    y[2 * i] = mode == 1 ? __fsub_rn(a0, b0) : __fadd_rn(a0, b0);
-    y[2 * i + 1] = mode == 1 ? __fsub_rn(a1, b1) : __fadd_rn(a1, b1);
+    for (int i = 0; i < 4; ++i) y[i] = add2(mul2(y[i], c[i]), mul2(z[i], s[i]));
   }
+}
+
+// Largest magnitude of three; NaN if one is.
+__device__ __forceinline__ float max_abs(float a, float b, float c) {
+  float y;
+  asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+  return y;
 }
 
 // MXFP4 of 8 coordinates; the 4 lanes of an aligned quad hold one block of 32. The scale
-// comes from the largest magnitude's exponent alone, read off its bits (as integers, NaN >
-// infinity > every finite value), so it is exact; x 2^-e is exact as well unless it falls
-// far below the smallest code.
-__device__ __forceinline__ uint32_t quantise8(const float (&y)[8], uint32_t& scale) {
-  uint32_t m = 0;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(y[i]) & 0x7fffffffu);
-  m = max(m, __shfl_xor_sync(kFull, m, 1));
-  m = max(m, __shfl_xor_sync(kFull, m, 2));
-  if (m >= 0x7f800000u) {
-    scale = 255;
-    return 0;
-  }
+// comes from the largest magnitude's exponent alone, read off its bits (NaN > infinity > every
+// finite value as integers), so it is exact; x 2^-e is exact as well unless it falls far below
+// the smallest code.
+__device__ __forceinline__ uint32_t quantise8(const float2 (&y)[4], uint32_t& scale) {
+  float f = max_abs(max_abs(y[0].x, y[0].y, y[1].x), max_abs(y[1].y, y[2].x, y[2].y), max_abs(y[3].x, y[3].y, 0.f));
+  f = max_abs(f, __shfl_xor_sync(kFull, f, 1), f);
+  f = max_abs(f, __shfl_xor_sync(kFull, f, 2), f);
+  const uint32_t m = __float_as_uint(f);
   const int e = max((int)(m >> 23) - 127 - 2, -126);
-  scale = (uint32_t)(e + 127);
-  const float r = __uint_as_float((uint32_t)(127 - e) << 23);
-  uint32_t w = 0;
+  const bool finite = m < 0x7f800000u;
+  scale = finite ? (uint32_t)(e + 127) : 255u;
+  const float r = finite ? __uint_as_float((uint32_t)(127 - e) << 23) : 0.f;
+  const float2 r2 = make_float2(r, r);
+  uint32_t b[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) w |= e2m1_pair(y[2 * i] * r, y[2 * i + 1] * r) << (8 * i);
-  return w;
+  for (int i = 0; i < 4; ++i) {
+    const float2 z = sm100::mul2(y[i], r2);
+    b[i] = e2m1_pair(z.x, z.y);
+  }
+  return finite ? __byte_perm(__byte_perm(b[0], b[1], 0x5540), __byte_perm(b[2], b[3], 0x5540), 0x5410) : 0u;
 }
 
+// A group: VP = 32 / LPV consecutive heads of a token's queries, keys or values, one warp's lanes
+// wide. Groups are numbered over queries, then keys, then values, each rounded up to whole groups.
 template <typename T, bool MX, int LPV>
 __global__ void __launch_bounds__(kThreads) append_kernel(const AppendArgs a) {
-  constexpr int VP = 32 / LPV;  // vectors a warp holds at once
+  constexpr int VP = 32 / LPV;
+  constexpr int kVec = LPV * 16;  // bytes of a vector
   const int lane = threadIdx.x & 31;
   const int64_t wid = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
-  const int64_t tok = wid / a.splits;
+  const int64_t tok = quotient(wid, a.splits);
   if (tok >= a.n) return;
   const int split = (int)(wid - tok * a.splits);
   const int ch = lane % LPV, sub = lane / LPV;
   const PageView& pg = a.pg;
   const int64_t* slots = a.slot + (pg.per_head ? tok * pg.hkv : tok);
   const int64_t slot0 = __ldg(slots);
-  if (!pg.per_head && slot0 == -1) return;
-  const int heads = a.hq + 2 * pg.hkv;
+  const int64_t pos = a.half ? __ldg(a.pos + tok) : 0;
+  const int gq = (a.hq + VP - 1) / VP, gk = (pg.hkv + VP - 1) / VP, groups = gq + 2 * gk;
+  const int g0 = split * a.iters, g1 = min(groups, g0 + a.iters);
 
-  // the rotation of this lane's chunk
-  int mode = 0, pch = ch;
-  float c[8], s[8];
-  if (a.half) {
-    if (pg.per_head) {  // a row whose every slot is padding has no position
-      bool any = false;
-      for (int h = 0; h < pg.hkv; ++h) any |= __ldg(slots + h) != -1;
-      if (!any) return;
+  // the rotated part of a vector, and the chunk with the pairs' other coordinates
+  const bool rotated = ch * 8 < 2 * a.half;
+  const bool first_half = ch * 8 < a.half;
+  const int pch = a.interleaved || !rotated ? ch : first_half ? ch + a.half / 8 : ch - a.half / 8;
+  uint4 own[kUnroll], par[kUnroll];
+  auto load = [&](int g) {
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      own[u] = par[u] = make_uint4(0, 0, 0, 0);
+      const int gu = g + u;
+      if (gu >= g1) continue;
+      const bool is_q = gu < gq, is_k = !is_q && gu < gq + gk;
+      const int h = (gu - (is_q ? 0 : is_k ? gq : gq + gk)) * VP + sub;
+      if (h >= (is_q ? a.hq : pg.hkv)) continue;
+      const char* src = (is_q ? a.q + tok * a.q_b : is_k ? a.k + tok * a.k_b : a.v + tok * a.v_b) + h * kVec;
+      own[u] = *reinterpret_cast<const uint4*>(src + ch * 16);
+      if ((is_q || is_k) && pch != ch) par[u] = *reinterpret_cast<const uint4*>(src + pch * 16);
     }
-    const int64_t pos = __ldg(a.pos + tok);
+  };
+  load(g0);  // on their way before the slot, the position and then the table's row are known
+
+  if (pg.per_head) {  // a row whose every slot is padding has no position
+    bool any = false;
+    for (int h = 0; h < pg.hkv; ++h) any |= __ldg(slots + h) != -1;
+    if (!any) return;
+  } else if (slot0 == -1) {
+    return;
+  }
+  float2 c[4], s[4];
+  if (a.half) {
     if (pos < 0 || pos >= a.n_pos) {
       if (lane == 0) atomicOr(a.err, kErrIndex);
       return;
     }
-    if (ch * 8 < 2 * a.half) {
-      const float* row = a.table + pos * 2 * a.half;
-      if (a.interleaved) {
-        mode = 3;
-        const float4 x = __ldg(reinterpret_cast<const float4*>(row + ch * 4));
-        const float4 y = __ldg(reinterpret_cast<const float4*>(row + a.half + ch * 4));
-        c[0] = x.x, c[1] = x.y, c[2] = x.z, c[3] = x.w;
-        s[0] = y.x, s[1] = y.y, s[2] = y.z, s[3] = y.w;
-      } else {
-        mode = ch * 8 < a.half ? 1 : 2;
-        pch = mode == 1 ? ch + a.half / 8 : ch - a.half / 8;
-        const int t0 = (mode == 1 ? ch : pch) * 8;
+    if (rotated && g0 < gq + gk) {
+      const float* row = a.table + pos * 2 * a.half + (a.interleaved ? ch * 4 : (first_half ? ch : pch) * 8);
+      const float sg = a.interleaved || !first_half ? 1.f : -1.f;
 #pragma unroll
-        for (int i = 0; i < 8; i += 4) {
-          const float4 x = __ldg(reinterpret_cast<const float4*>(row + t0 + i));
-          const float4 y = __ldg(reinterpret_cast<const float4*>(row + a.half + t0 + i));
-          c[i] = x.x, c[i + 1] = x.y, c[i + 2] = x.z, c[i + 3] = x.w;
-          s[i] = y.x, s[i + 1] = y.y, s[i + 2] = y.z, s[i + 3] = y.w;
-        }
+      for (int i = 0; i < 2; ++i) {
+        if (a.interleaved && i) break;
+        const float4 x = __ldg(reinterpret_cast<const float4*>(row + 4 * i));
+        const float4 y = __ldg(reinterpret_cast<const float4*>(row + a.half + 4 * i));
+        c[2 * i] = make_float2(x.x, x.y), c[2 * i + 1] = make_float2(x.z, x.w);
+        s[2 * i] = make_float2(sg * y.x, sg * y.y), s[2 * i + 1] = make_float2(sg * y.z, sg * y.w);
       }
     }
   }
@@ -153,54 +175,44 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const AppendArgs a) {
   int64_t soff0 = 0;  // the row's place in the cache, where its heads share one
   const bool in0 = slot0 >= 0 && slot0 < pg.n_slots;
   const int64_t off0 = !pg.per_head && in0 ? record_offset(pg, slot0, 0, soff0) : 0;
-
-  const int first = split * a.iters * VP + sub;
-  for (int i0 = 0; i0 < a.iters; i0 += kUnroll) {
-    uint4 own[kUnroll], par[kUnroll];
-#pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      const int h = first + (i0 + u) * VP;
-      own[u] = par[u] = make_uint4(0, 0, 0, 0);
-      if (i0 + u >= a.iters || h >= heads) continue;
-      const char* src = h < a.hq                ? a.q + tok * a.q_b + (int64_t)h * (LPV * 16)
-                        : h < a.hq + pg.hkv     ? a.k + tok * a.k_b + (int64_t)(h - a.hq) * (LPV * 16)
-                                                : a.v + tok * a.v_b + (int64_t)(h - a.hq - pg.hkv) * (LPV * 16);
-      own[u] = *reinterpret_cast<const uint4*>(src + ch * 16);
-      if (h < a.hq + pg.hkv && (mode == 1 || mode == 2)) par[u] = *reinterpret_cast<const uint4*>(src + pch * 16);
-    }
+  for (int g = g0; g < g1; g += kUnroll) {
+    if (g != g0) load(g);
     __syncwarp();  // q_out may be q: every chunk is read before any is written
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
-      const int h = first + (i0 + u) * VP;
-      const bool live = i0 + u < a.iters && h < heads;
-      const bool is_q = h < a.hq;
-      float y[8];
-      turn<T>(own[u], par[u], h < a.hq + pg.hkv ? mode : 0, c, s, y);
-      uint32_t word = 0, scale = 0;
-      if constexpr (MX) word = quantise8(y, scale);  // warp-wide: before any lane leaves
-      if (!live) continue;
-      const uint4 packed = make_uint4(Half2<T>::pack(y[0], y[1]), Half2<T>::pack(y[2], y[3]),
-                                      Half2<T>::pack(y[4], y[5]), Half2<T>::pack(y[6], y[7]));
+      const int gu = g + u;
+      if (gu >= g1) break;
+      const bool is_q = gu < gq, is_k = !is_q && gu < gq + gk;
+      const int h = (gu - (is_q ? 0 : is_k ? gq : gq + gk)) * VP + sub;
+      const bool live = h < (is_q ? a.hq : pg.hkv);
+      float2 y[4];
+      unpack8<T>(own[u], y);
+      if ((is_q || is_k) && rotated) turn<T>(y, par[u], a.interleaved, c, s);
       if (is_q) {
-        if (slot0 != -1)
-          *reinterpret_cast<uint4*>(a.q_out + tok * a.qo_b + (int64_t)h * (LPV * 16) + ch * 16) = packed;
+        if (live && slot0 != -1)
+          *reinterpret_cast<uint4*>(a.q_out + tok * a.qo_b + h * kVec + ch * 16) =
+              make_uint4(Half2<T>::pack(y[0].x, y[0].y), Half2<T>::pack(y[1].x, y[1].y),
+                         Half2<T>::pack(y[2].x, y[2].y), Half2<T>::pack(y[3].x, y[3].y));
         continue;
       }
-      const bool is_k = h < a.hq + pg.hkv;
-      const int kh = is_k ? h - a.hq : h - a.hq - pg.hkv;
-      const int64_t slot = pg.per_head ? __ldg(slots + kh) : slot0;
+      uint32_t word = 0, scale = 0;
+      if constexpr (MX) word = quantise8(y, scale);  // warp-wide: groups are of one kind
+      if (!live) continue;
+      const int64_t slot = pg.per_head ? __ldg(slots + h) : slot0;
       if (slot < 0 || slot >= pg.n_slots) {
         if (slot != -1 && ch == 0) atomicOr(a.err, kErrIndex);
         continue;
       }
-      int64_t off = off0 + (int64_t)kh * pg.head_b, soff = soff0 + (int64_t)kh * pg.shead_b;
-      if (pg.per_head) off = record_offset(pg, slot, kh, soff);
+      int64_t off = off0 + (int64_t)h * pg.head_b, soff = soff0 + (int64_t)h * pg.shead_b;
+      if (pg.per_head) off = record_offset(pg, slot, h, soff);
       char* base = is_k ? pg.k : pg.v;
       if constexpr (MX) {
         *reinterpret_cast<uint32_t*>(base + off + ch * 4) = word;
         if ((ch & 3) == 0) (is_k ? pg.ks : pg.vs)[soff + ch / 4] = (uint8_t)scale;
       } else {
-        *reinterpret_cast<uint4*>(base + off + ch * 16) = packed;
+        *reinterpret_cast<uint4*>(base + off + ch * 16) =
+            make_uint4(Half2<T>::pack(y[0].x, y[0].y), Half2<T>::pack(y[1].x, y[1].y),
+                       Half2<T>::pack(y[2].x, y[2].y), Half2<T>::pack(y[3].x, y[3].y));
       }
     }
   }
@@ -212,41 +224,56 @@ struct ReadArgs {
   int64_t n;
   char* k_out;
   char* v_out;
+  int splits, iters;  // warps per token, groups of 32 / LPV heads per warp
   unsigned int* err;
 };
 
-// One lane per 16-byte chunk of the dense rows; blockIdx.y 0: keys, 1: values (or the one
-// output asked for). kUnroll chunks of a lane lie a grid apart and are in flight together.
+// A warp reads groups of VP heads of one token, LPV lanes a vector, kReads groups in flight;
+// blockIdx.y 0: keys, 1: values (or the one output asked for).
+constexpr int kReads = 4;
 template <bool MX, int LPV>
 __global__ void __launch_bounds__(kThreads) read_kernel(const ReadArgs a) {
+  constexpr int VP = 32 / LPV;
   const PageView& pg = a.pg;
   const bool keys = a.k_out && (blockIdx.y == 0);
   const char* base = keys ? pg.k : pg.v;
   const uint8_t* sbase = keys ? pg.ks : pg.vs;
-  char* out = keys ? a.k_out : a.v_out;
-  const int64_t total = a.n * pg.hkv * LPV, step = (int64_t)gridDim.x * kThreads;
-  for (int64_t c0 = (int64_t)blockIdx.x * kThreads + threadIdx.x; c0 < total; c0 += step * kUnroll) {
-    int64_t slot[kUnroll];
-    uint4 x[kUnroll];
-    uint32_t sc[kUnroll];
-#pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      const int64_t vec = (c0 + u * step) / LPV;
-      slot[u] = c0 + u * step < total ? __ldg(a.slot + (pg.per_head ? vec : quotient(vec, pg.hkv))) : -1;
+  const int lane = threadIdx.x & 31, ch = lane % LPV;
+  const int64_t wid = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
+  const int64_t tok = quotient(wid, a.splits);
+  if (tok >= a.n) return;
+  const int split = (int)(wid - tok * a.splits);
+  char* out = (keys ? a.k_out : a.v_out) + tok * pg.hkv * (LPV * 16) + ch * 16;
+  const int64_t* slots = a.slot + (pg.per_head ? tok * pg.hkv : tok);
+  const int h0 = split * a.iters * VP, h1 = min(pg.hkv, h0 + a.iters * VP);
+  int64_t off0 = 0, soff0 = 0;
+  if (!pg.per_head) {
+    const int64_t slot = __ldg(slots);
+    if (slot < 0 || slot >= pg.n_slots) {
+      if (slot != -1 && lane == 0) atomicOr(a.err, kErrIndex);
+      return;
     }
+    off0 = record_offset(pg, slot, 0, soff0);
+  }
+  for (int hb = h0 + lane / LPV; hb < h1; hb += kReads * VP) {
+    uint4 x[kReads];
+    uint32_t sc[kReads];
+    bool ok[kReads];
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      x[u] = make_uint4(0, 0, 0, 0);
-      sc[u] = 0;
-      if (slot[u] < 0 || slot[u] >= pg.n_slots) {
-        if (slot[u] != -1) atomicOr(a.err, kErrIndex);
-        slot[u] = -1;
-        continue;
+    for (int u = 0; u < kReads; ++u) {
+      const int h = hb + u * VP;
+      ok[u] = h < h1;
+      if (!ok[u]) continue;
+      int64_t off = off0 + (int64_t)h * pg.head_b, soff = soff0 + (int64_t)h * pg.shead_b;
+      if (pg.per_head) {
+        const int64_t slot = __ldg(slots + h);
+        ok[u] = slot >= 0 && slot < pg.n_slots;
+        if (!ok[u]) {
+          if (slot != -1 && ch == 0) atomicOr(a.err, kErrIndex);
+          continue;
+        }
+        off = record_offset(pg, slot, h, soff);
       }
-      const int64_t c = c0 + u * step, vec = c / LPV;
-      const int ch = (int)(c - vec * LPV);
-      int64_t soff;
-      const int64_t off = record_offset(pg, slot[u], (int)(vec - quotient(vec, pg.hkv) * pg.hkv), soff);
       if constexpr (MX) {
         x[u].x = *reinterpret_cast<const uint32_t*>(base + off + ch * 4);
         sc[u] = sbase[soff + ch / 4];
@@ -255,20 +282,20 @@ __global__ void __launch_bounds__(kThreads) read_kernel(const ReadArgs a) {
       }
     }
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      if (slot[u] < 0) continue;
+    for (int u = 0; u < kReads; ++u) {
+      if (!ok[u]) continue;
       if constexpr (MX) {
         uint32_t h[4], r[4];
         e2m1x8_f16(x[u].x, h);
         const float f = e8m0(sc[u]);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const float2 t = Half2<__half>::unpack(h[i]);
-          r[i] = Half2<__nv_bfloat16>::pack(t.x * f, t.y * f);
+          const float2 t = sm100::mul2(Half2<__half>::unpack(h[i]), make_float2(f, f));
+          r[i] = Half2<__nv_bfloat16>::pack(t.x, t.y);
         }
         x[u] = make_uint4(r[0], r[1], r[2], r[3]);
       }
-      *reinterpret_cast<uint4*>(out + (c0 + u * step) * 16) = x[u];
+      *reinterpret_cast<uint4*>(out + (int64_t)(hb + u * VP) * (LPV * 16)) = x[u];
     }
   }
 }
@@ -297,13 +324,14 @@ cudaError_t launch_kv_append(const tq_ctx* ctx, const PageView& pg, int format, 
     a.half = rope->rot_dim / 2, a.interleaved = rope->interleaved;
   }
   a.slot = slot, a.n = n, a.hq = q ? hq : 0, a.err = ctx->d_err;
-  // Heads per warp: one group of 32 / (d / 8) vectors each while that leaves the SMs short of
-  // warps (a decode step is latency), more as tokens grow, up to 8 groups, so that a warp's
-  // table row serves several heads.
-  const int vp = 256 / ctx->shape.d, groups = (a.hq + 2 * pg.hkv + vp - 1) / vp;
-  const int64_t want = (int64_t)ctx->num_sms * 64;
-  a.iters = (int)std::max<int64_t>(1, std::min<int64_t>(8, n * groups / want));
-  a.splits = (groups + a.iters - 1) / a.iters;
+  // Groups per warp: one while that leaves the SMs short of warps (a decode step is latency), more
+  // as tokens grow, so that the row of the rotation table, four times a vector's bytes, serves
+  // several heads.
+  const int vp = 256 / ctx->shape.d, groups = (a.hq + vp - 1) / vp + 2 * ((pg.hkv + vp - 1) / vp);
+  const int64_t want = (int64_t)ctx->num_sms * 32;
+  const int most = (int)std::max<int64_t>(1, std::min<int64_t>(kMostGroups, n * groups / want));
+  a.splits = (groups + most - 1) / most;
+  a.iters = (groups + a.splits - 1) / a.splits;
   const int64_t blocks = (n * a.splits + kThreads / 32 - 1) / (kThreads / 32);
   if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
   if (format == TQ_KV_MXFP4) return run_append<__nv_bfloat16, true>(ctx->shape.d, a, (unsigned)blocks, stream);
@@ -313,13 +341,14 @@ cudaError_t launch_kv_append(const tq_ctx* ctx, const PageView& pg, int format, 
 
 cudaError_t launch_kv_read(const tq_ctx* ctx, const PageView& pg, int format, int64_t n, const int64_t* slot,
                            void* k_out, void* v_out, cudaStream_t stream) {
-  const ReadArgs a{pg, slot, n, static_cast<char*>(k_out), static_cast<char*>(v_out), ctx->d_err};
-  const int lpv = ctx->shape.d / 8;
-  const int64_t chunks = n * pg.hkv * lpv;
-  // one chunk per lane until the grid holds 8 blocks per SM, then up to kUnroll
-  const int64_t most = (int64_t)ctx->num_sms * 8;
-  const int64_t need = (chunks + kThreads - 1) / kThreads;
-  const int64_t blocks = std::min(need, std::max(most, (need + kUnroll - 1) / kUnroll));
+  ReadArgs a{pg, slot, n, static_cast<char*>(k_out), static_cast<char*>(v_out), 1, 1, ctx->d_err};
+  const int lpv = ctx->shape.d / 8, vp = 32 / lpv, groups = (pg.hkv + vp - 1) / vp;
+  // one group per warp until the SMs hold 32 warps each, then up to the kReads in flight
+  const int64_t want = (int64_t)ctx->num_sms * 32;
+  const int most = (int)std::max<int64_t>(1, std::min<int64_t>(kReads, n * groups / want));
+  a.splits = (groups + most - 1) / most;
+  a.iters = (groups + a.splits - 1) / a.splits;
+  const int64_t blocks = (n * a.splits + kThreads / 32 - 1) / (kThreads / 32);
   if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
   const dim3 grid((unsigned)blocks, k_out && v_out ? 2 : 1);
   const bool mx = format == TQ_KV_MXFP4;

@@ -17,7 +17,8 @@ __device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
 
 // Byte offset of cache row `slot`'s record for KV head h; `soff` its scale bytes'.
 __device__ __forceinline__ int64_t record_offset(const PageView& p, int64_t slot, int h, int64_t& soff) {
-  const int64_t pg = quotient(slot, p.page_size), t = slot - pg * p.page_size;
+  const int64_t pg = p.page_shift >= 0 ? slot >> p.page_shift : quotient(slot, p.page_size);
+  const int64_t t = slot - pg * p.page_size;
   soff = pg * p.spage_b + t * p.stok_b + (int64_t)h * p.shead_b;
   return pg * p.page_b + t * p.tok_b + (int64_t)h * p.head_b;
 }

@@ -165,6 +165,7 @@ struct PageView {
   int64_t page_b, tok_b, head_b;     // record strides in bytes
   int64_t spage_b, stok_b, shead_b;  // scale strides in bytes
   int64_t page_size, n_pages, n_slots;
+  int page_shift;                    // log2 of page_size, or -1
   int hkv;
   int per_head;
 };
