@@ -6,9 +6,10 @@
 // rounding to the 16-bit type or to MXFP4. read: records back to dense rows.
 //
 // Both move each byte once and are bound by HBM, or by launch latency for a decode step.
-// A lane owns one 16-byte chunk (8 coordinates) of a vector, so a vector is d / 8 lanes and
-// its loads and stores are whole lines; the partner chunk of the half-split rotation is a
-// second load of the same lines (an L1 hit), which costs less than exchanging 4 registers.
+// A lane owns one 16-byte chunk (8 coordinates) of a vector, so a vector is d / 8 lanes of a warp
+// and its loads and stores are whole lines; the partner chunk of the half-split rotation comes
+// from its lane by shuffles (a second load of it would hold its registers over the memory's
+// latency: 92 per thread instead of 64, and fewer warps to hide that latency).
 // A warp keeps the 8 cosines and 8 sines of its chunk in registers and walks the heads of
 // one token with them: the table's 4 rot_dim bytes per token are read once per warp and not
 // once per head (the table bytes of a chunk are four times its data).
@@ -32,18 +33,17 @@ struct AppendArgs {
   const int64_t* pos;
   int64_t n_pos;
   int half;  // rot_dim / 2; 0: no rotation
-  int interleaved;
   const int64_t* slot;
   int64_t n;
   int hq;       // 0: no queries
-  int splits;   // warps that share a token
-  int iters;    // vectors each lane handles
+  int q_blocks, kv_blocks;  // blocks of the queries, and of the keys as of the values
+  int q_splits, kv_splits;  // warps that share a token
+  int q_iters, kv_iters;    // groups of heads per warp
   unsigned int* err;
 };
 
 constexpr int kThreads = 256;
-constexpr int kUnroll = 2;      // vectors in flight per lane
-constexpr int kMostGroups = 8;  // most groups (see append_kernel) per warp
+constexpr int kMostGroups = 8;  // most groups of heads per warp
 
 // The 8 coordinates of a chunk as fp32.
 template <typename T>
@@ -55,11 +55,10 @@ __device__ __forceinline__ void unpack8(const uint4& x, float2 (&y)[4]) {
 // Rotate a chunk in place. Halves: its own coordinates times cosines plus the pairs' others times
 // signed sines (-sin where the chunk holds the first coordinates: a c + b (-s) rounds like
 // a c - b s). Interleaved: the pairs lie in the chunk, c and s hold their four angles.
-template <typename T>
-__device__ __forceinline__ void turn(float2 (&y)[4], const uint4& par, bool interleaved, const float2 (&c)[4],
-                                     const float2 (&s)[4]) {
+template <typename T, bool INTER, int N>
+__device__ __forceinline__ void turn(float2 (&y)[4], const uint4& par, const float2 (&c)[N], const float2 (&s)[N]) {
   using namespace sm100;
-  if (interleaved) {
+  if constexpr (INTER) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const float ci = i & 1 ? c[i / 2].y : c[i / 2].x, si = i & 1 ? s[i / 2].y : s[i / 2].x;
@@ -105,45 +104,46 @@ __device__ __forceinline__ uint32_t quantise8(const float2 (&y)[4], uint32_t& sc
   return finite ? __byte_perm(__byte_perm(b[0], b[1], 0x5540), __byte_perm(b[2], b[3], 0x5540), 0x5410) : 0u;
 }
 
-// A group: VP = 32 / LPV consecutive heads of a token's queries, keys or values, one warp's lanes
-// wide. Groups are numbered over queries, then keys, then values, each rounded up to whole groups.
-template <typename T, bool MX, int LPV>
-__global__ void __launch_bounds__(kThreads) append_kernel(const AppendArgs a) {
+// A block works on one kind: queries, keys or values (in this order of blocks). A warp takes
+// `iters` groups of VP = 32 / LPV heads of one token, all lanes wide.
+template <typename T, bool MX, int LPV, bool INTER>
+__global__ void __launch_bounds__(kThreads, INTER ? 4 : 3) append_kernel(const AppendArgs a) {
   constexpr int VP = 32 / LPV;
   constexpr int kVec = LPV * 16;  // bytes of a vector
-  const int lane = threadIdx.x & 31;
-  const int64_t wid = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
-  const int64_t tok = quotient(wid, a.splits);
-  if (tok >= a.n) return;
-  const int split = (int)(wid - tok * a.splits);
-  const int ch = lane % LPV, sub = lane / LPV;
+  // vectors in flight per lane, blocks per SM: what the registers allow (a rotation by halves holds
+  // 16 cosines and sines and the partner chunk); at 64 registers the latter spills
+  constexpr int kUnroll = INTER ? 4 : 2;
   const PageView& pg = a.pg;
+  const int lane = threadIdx.x & 31, ch = lane % LPV, sub = lane / LPV;
+  int block = blockIdx.x;
+  const bool is_q = block < a.q_blocks;
+  const bool is_k = !is_q && block < a.q_blocks + a.kv_blocks;
+  block -= is_q ? 0 : is_k ? a.q_blocks : a.q_blocks + a.kv_blocks;
+  const int heads = is_q ? a.hq : pg.hkv, splits = is_q ? a.q_splits : a.kv_splits;
+  const int64_t wid = (int64_t)block * (kThreads / 32) + (threadIdx.x >> 5);
+  const int64_t tok = quotient(wid, splits);
+  if (tok >= a.n) return;
+  const int iters = is_q ? a.q_iters : a.kv_iters, h0 = (int)(wid - tok * splits) * iters * VP + sub;
+  const int h1 = min(heads, h0 - sub + iters * VP);
   const int64_t* slots = a.slot + (pg.per_head ? tok * pg.hkv : tok);
   const int64_t slot0 = __ldg(slots);
+  const bool turned = a.half && (is_q || is_k);
   const int64_t pos = a.half ? __ldg(a.pos + tok) : 0;
-  const int gq = (a.hq + VP - 1) / VP, gk = (pg.hkv + VP - 1) / VP, groups = gq + 2 * gk;
-  const int g0 = split * a.iters, g1 = min(groups, g0 + a.iters);
 
-  // the rotated part of a vector, and the chunk with the pairs' other coordinates
-  const bool rotated = ch * 8 < 2 * a.half;
+  // the rotated part of a vector, and the lane with the pairs' other coordinates
+  const bool rotated = turned && ch * 8 < 2 * a.half;
   const bool first_half = ch * 8 < a.half;
-  const int pch = a.interleaved || !rotated ? ch : first_half ? ch + a.half / 8 : ch - a.half / 8;
-  uint4 own[kUnroll], par[kUnroll];
-  auto load = [&](int g) {
+  const int peer = INTER || !rotated ? lane : first_half ? lane + a.half / 8 : lane - a.half / 8;
+  const char* src = (is_q ? a.q + tok * a.q_b : is_k ? a.k + tok * a.k_b : a.v + tok * a.v_b) + ch * 16;
+  uint4 own[kUnroll];
+  auto load = [&](int h) {
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
-      own[u] = par[u] = make_uint4(0, 0, 0, 0);
-      const int gu = g + u;
-      if (gu >= g1) continue;
-      const bool is_q = gu < gq, is_k = !is_q && gu < gq + gk;
-      const int h = (gu - (is_q ? 0 : is_k ? gq : gq + gk)) * VP + sub;
-      if (h >= (is_q ? a.hq : pg.hkv)) continue;
-      const char* src = (is_q ? a.q + tok * a.q_b : is_k ? a.k + tok * a.k_b : a.v + tok * a.v_b) + h * kVec;
-      own[u] = *reinterpret_cast<const uint4*>(src + ch * 16);
-      if ((is_q || is_k) && pch != ch) par[u] = *reinterpret_cast<const uint4*>(src + pch * 16);
+      own[u] = make_uint4(0, 0, 0, 0);
+      if (h + u * VP < h1) own[u] = *reinterpret_cast<const uint4*>(src + (h + u * VP) * kVec);
     }
   };
-  load(g0);  // on their way before the slot, the position and then the table's row are known
+  load(h0);  // on their way before the slot, the position and then the table's row are known
 
   if (pg.per_head) {  // a row whose every slot is padding has no position
     bool any = false;
@@ -152,65 +152,73 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const AppendArgs a) {
   } else if (slot0 == -1) {
     return;
   }
-  float2 c[4], s[4];
+  constexpr int NT = INTER ? 2 : 4;  // an interleaved chunk has four angles
+  float2 c[NT], s[NT];
   if (a.half) {
     if (pos < 0 || pos >= a.n_pos) {
       if (lane == 0) atomicOr(a.err, kErrIndex);
       return;
     }
-    if (rotated && g0 < gq + gk) {
-      const float* row = a.table + pos * 2 * a.half + (a.interleaved ? ch * 4 : (first_half ? ch : pch) * 8);
-      const float sg = a.interleaved || !first_half ? 1.f : -1.f;
+    if (rotated) {
+      const float* row = a.table + pos * 2 * a.half + (INTER ? ch * 4 : first_half ? ch * 8 : ch * 8 - a.half);
+      const float sg = !INTER && first_half ? -1.f : 1.f;
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        if (a.interleaved && i) break;
-        const float4 x = __ldg(reinterpret_cast<const float4*>(row + 4 * i));
-        const float4 y = __ldg(reinterpret_cast<const float4*>(row + a.half + 4 * i));
-        c[2 * i] = make_float2(x.x, x.y), c[2 * i + 1] = make_float2(x.z, x.w);
-        s[2 * i] = make_float2(sg * y.x, sg * y.y), s[2 * i + 1] = make_float2(sg * y.z, sg * y.w);
+      for (int i = 0; i < NT; i += 2) {
+        const float4 x = __ldg(reinterpret_cast<const float4*>(row + 2 * i));
+        const float4 y = __ldg(reinterpret_cast<const float4*>(row + a.half + 2 * i));
+        c[i] = make_float2(x.x, x.y), c[i + 1] = make_float2(x.z, x.w);
+        s[i] = make_float2(sg * y.x, sg * y.y), s[i + 1] = make_float2(sg * y.z, sg * y.w);
       }
     }
   }
 
-  int64_t soff0 = 0;  // the row's place in the cache, where its heads share one
-  const bool in0 = slot0 >= 0 && slot0 < pg.n_slots;
-  const int64_t off0 = !pg.per_head && in0 ? record_offset(pg, slot0, 0, soff0) : 0;
-  for (int g = g0; g < g1; g += kUnroll) {
-    if (g != g0) load(g);
+  int64_t off0 = 0, soff0 = 0;  // the row's place in the cache, where its heads share one
+  if (!is_q && !pg.per_head) {
+    if (slot0 < 0 || slot0 >= pg.n_slots) {
+      if (lane == 0) atomicOr(a.err, kErrIndex);
+      return;
+    }
+    off0 = record_offset<MX>(pg, slot0, soff0);
+  }
+  char* dst = is_q ? a.q_out + tok * a.qo_b + ch * 16 : (is_k ? pg.k : pg.v) + off0 + ch * (MX ? 4 : 16);
+  for (int h = h0; h - sub < h1; h += kUnroll * VP) {
+    if (h != h0) load(h);
     __syncwarp();  // q_out may be q: every chunk is read before any is written
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
-      const int gu = g + u;
-      if (gu >= g1) break;
-      const bool is_q = gu < gq, is_k = !is_q && gu < gq + gk;
-      const int h = (gu - (is_q ? 0 : is_k ? gq : gq + gk)) * VP + sub;
-      const bool live = h < (is_q ? a.hq : pg.hkv);
+      const int hu = h + u * VP;
+      if (hu - sub >= h1) break;
       float2 y[4];
       unpack8<T>(own[u], y);
-      if ((is_q || is_k) && rotated) turn<T>(y, par[u], a.interleaved, c, s);
-      if (is_q) {
-        if (live && slot0 != -1)
-          *reinterpret_cast<uint4*>(a.q_out + tok * a.qo_b + h * kVec + ch * 16) =
-              make_uint4(Half2<T>::pack(y[0].x, y[0].y), Half2<T>::pack(y[1].x, y[1].y),
-                         Half2<T>::pack(y[2].x, y[2].y), Half2<T>::pack(y[3].x, y[3].y));
-        continue;
+      uint4 par = own[u];
+      if (!INTER && turned) {
+        par.x = __shfl_sync(kFull, par.x, peer), par.y = __shfl_sync(kFull, par.y, peer);
+        par.z = __shfl_sync(kFull, par.z, peer), par.w = __shfl_sync(kFull, par.w, peer);
       }
+      if (rotated) turn<T, INTER>(y, par, c, s);
       uint32_t word = 0, scale = 0;
-      if constexpr (MX) word = quantise8(y, scale);  // warp-wide: groups are of one kind
-      if (!live) continue;
-      const int64_t slot = pg.per_head ? __ldg(slots + h) : slot0;
-      if (slot < 0 || slot >= pg.n_slots) {
-        if (slot != -1 && ch == 0) atomicOr(a.err, kErrIndex);
-        continue;
+      if constexpr (MX)
+        if (!is_q) word = quantise8(y, scale);  // by all lanes of a warp
+      if (hu >= h1) continue;
+      int64_t off = hu * kVec, soff = soff0;
+      if (is_q) {
+        if (slot0 == -1) continue;  // per-head pages: KV head 0's slot speaks for the queries
+      } else if (!pg.per_head) {
+        off = times(hu, pg.head_b);
+        if constexpr (MX) soff += times(hu, pg.shead_b);
+      } else {
+        const int64_t slot = __ldg(slots + hu);
+        if (slot < 0 || slot >= pg.n_slots) {
+          if (slot != -1 && ch == 0) atomicOr(a.err, kErrIndex);
+          continue;
+        }
+        off = record_offset<MX>(pg, slot, soff);
       }
-      int64_t off = off0 + (int64_t)h * pg.head_b, soff = soff0 + (int64_t)h * pg.shead_b;
-      if (pg.per_head) off = record_offset(pg, slot, h, soff);
-      char* base = is_k ? pg.k : pg.v;
-      if constexpr (MX) {
-        *reinterpret_cast<uint32_t*>(base + off + ch * 4) = word;
+      if (MX && !is_q) {
+        *reinterpret_cast<uint32_t*>(dst + off) = word;
         if ((ch & 3) == 0) (is_k ? pg.ks : pg.vs)[soff + ch / 4] = (uint8_t)scale;
       } else {
-        *reinterpret_cast<uint4*>(base + off + ch * 16) =
+        *reinterpret_cast<uint4*>(dst + off) =
             make_uint4(Half2<T>::pack(y[0].x, y[0].y), Half2<T>::pack(y[1].x, y[1].y),
                        Half2<T>::pack(y[2].x, y[2].y), Half2<T>::pack(y[3].x, y[3].y));
       }
@@ -253,7 +261,7 @@ __global__ void __launch_bounds__(kThreads) read_kernel(const ReadArgs a) {
       if (slot != -1 && lane == 0) atomicOr(a.err, kErrIndex);
       return;
     }
-    off0 = record_offset(pg, slot, 0, soff0);
+    off0 = record_offset<MX>(pg, slot, soff0);
   }
   for (int hb = h0 + lane / LPV; hb < h1; hb += kReads * VP) {
     uint4 x[kReads];
@@ -264,15 +272,17 @@ __global__ void __launch_bounds__(kThreads) read_kernel(const ReadArgs a) {
       const int h = hb + u * VP;
       ok[u] = h < h1;
       if (!ok[u]) continue;
-      int64_t off = off0 + (int64_t)h * pg.head_b, soff = soff0 + (int64_t)h * pg.shead_b;
-      if (pg.per_head) {
+      int64_t off, soff;
+      if (!pg.per_head) {
+        off = off0 + times(h, pg.head_b), soff = soff0 + times(h, pg.shead_b);
+      } else {
         const int64_t slot = __ldg(slots + h);
         ok[u] = slot >= 0 && slot < pg.n_slots;
         if (!ok[u]) {
           if (slot != -1 && ch == 0) atomicOr(a.err, kErrIndex);
           continue;
         }
-        off = record_offset(pg, slot, h, soff);
+        off = record_offset<MX>(pg, slot, soff);
       }
       if constexpr (MX) {
         x[u].x = *reinterpret_cast<const uint32_t*>(base + off + ch * 4);
@@ -300,12 +310,17 @@ __global__ void __launch_bounds__(kThreads) read_kernel(const ReadArgs a) {
   }
 }
 
-template <typename T, bool MX>
+template <typename T, bool MX, bool INTER>
 cudaError_t run_append(int d, const AppendArgs& a, unsigned blocks, cudaStream_t st) {
-  if (d == 64) append_kernel<T, MX, 8><<<blocks, kThreads, 0, st>>>(a);
-  else if (d == 128) append_kernel<T, MX, 16><<<blocks, kThreads, 0, st>>>(a);
-  else append_kernel<T, MX, 32><<<blocks, kThreads, 0, st>>>(a);
+  if (d == 64) append_kernel<T, MX, 8, INTER><<<blocks, kThreads, 0, st>>>(a);
+  else if (d == 128) append_kernel<T, MX, 16, INTER><<<blocks, kThreads, 0, st>>>(a);
+  else append_kernel<T, MX, 32, INTER><<<blocks, kThreads, 0, st>>>(a);
   return cudaGetLastError();
+}
+
+template <typename T, bool MX>
+cudaError_t pick_append(int d, const AppendArgs& a, int interleaved, unsigned blocks, cudaStream_t st) {
+  return interleaved ? run_append<T, MX, true>(d, a, blocks, st) : run_append<T, MX, false>(d, a, blocks, st);
 }
 
 }  // namespace
@@ -321,22 +336,25 @@ cudaError_t launch_kv_append(const tq_ctx* ctx, const PageView& pg, int format, 
   a.q_b = q_stride * 2, a.k_b = k_stride * 2, a.v_b = v_stride * 2, a.qo_b = q_out_stride * 2;
   if (rope && rope->rot_dim > 0) {
     a.table = rope->cos_sin, a.pos = rope->positions, a.n_pos = rope->n_positions;
-    a.half = rope->rot_dim / 2, a.interleaved = rope->interleaved;
+    a.half = rope->rot_dim / 2;
   }
   a.slot = slot, a.n = n, a.hq = q ? hq : 0, a.err = ctx->d_err;
   // Groups per warp: one while that leaves the SMs short of warps (a decode step is latency), more
   // as tokens grow, so that the row of the rotation table, four times a vector's bytes, serves
   // several heads.
-  const int vp = 256 / ctx->shape.d, groups = (a.hq + vp - 1) / vp + 2 * ((pg.hkv + vp - 1) / vp);
+  const int vp = 256 / ctx->shape.d, gq = (a.hq + vp - 1) / vp, gk = (pg.hkv + vp - 1) / vp;
   const int64_t want = (int64_t)ctx->num_sms * 32;
-  const int most = (int)std::max<int64_t>(1, std::min<int64_t>(kMostGroups, n * groups / want));
-  a.splits = (groups + most - 1) / most;
-  a.iters = (groups + a.splits - 1) / a.splits;
-  const int64_t blocks = (n * a.splits + kThreads / 32 - 1) / (kThreads / 32);
+  const int most = (int)std::max<int64_t>(1, std::min<int64_t>(kMostGroups, n * (gq + 2 * gk) / want));
+  a.q_splits = (gq + most - 1) / most, a.kv_splits = (gk + most - 1) / most;
+  a.q_iters = gq ? (gq + a.q_splits - 1) / a.q_splits : 0, a.kv_iters = (gk + a.kv_splits - 1) / a.kv_splits;
+  const int64_t per = kThreads / 32, qb = (n * a.q_splits + per - 1) / per, kb = (n * a.kv_splits + per - 1) / per;
+  const int64_t blocks = qb + 2 * kb;
   if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
-  if (format == TQ_KV_MXFP4) return run_append<__nv_bfloat16, true>(ctx->shape.d, a, (unsigned)blocks, stream);
-  if (dtype == TQ_BF16) return run_append<__nv_bfloat16, false>(ctx->shape.d, a, (unsigned)blocks, stream);
-  return run_append<__half, false>(ctx->shape.d, a, (unsigned)blocks, stream);
+  a.q_blocks = (int)qb, a.kv_blocks = (int)kb;
+  const int inter = a.half && rope->interleaved, d = ctx->shape.d;
+  if (format == TQ_KV_MXFP4) return pick_append<__nv_bfloat16, true>(d, a, inter, (unsigned)blocks, stream);
+  if (dtype == TQ_BF16) return pick_append<__nv_bfloat16, false>(d, a, inter, (unsigned)blocks, stream);
+  return pick_append<__half, false>(d, a, inter, (unsigned)blocks, stream);
 }
 
 cudaError_t launch_kv_read(const tq_ctx* ctx, const PageView& pg, int format, int64_t n, const int64_t* slot,

@@ -15,12 +15,17 @@ __device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
   return (a >> 32) == 0 ? (int64_t)((uint32_t)a / (uint32_t)b) : a / b;
 }
 
-// Byte offset of cache row `slot`'s record for KV head h; `soff` its scale bytes'.
-__device__ __forceinline__ int64_t record_offset(const PageView& p, int64_t slot, int h, int64_t& soff) {
-  const int64_t pg = p.page_shift >= 0 ? slot >> p.page_shift : quotient(slot, p.page_size);
-  const int64_t t = slot - pg * p.page_size;
-  soff = pg * p.spage_b + t * p.stok_b + (int64_t)h * p.shead_b;
-  return pg * p.page_b + t * p.tok_b + (int64_t)h * p.head_b;
+// a * b for 0 <= a < 2^32: half the instructions of a full 64-bit product.
+__device__ __forceinline__ int64_t times(uint32_t a, int64_t b) { return (int64_t)((uint64_t)a * (uint64_t)b); }
+
+// Byte offset of cache row `slot`'s record for KV head 0 (or the page's own head); `soff` its
+// scale bytes'. Pages and tokens fit 31 and 20 bits.
+template <bool MX>
+__device__ __forceinline__ int64_t record_offset(const PageView& p, int64_t slot, int64_t& soff) {
+  const uint32_t pg = (uint32_t)(p.page_shift >= 0 ? slot >> p.page_shift : quotient(slot, p.page_size));
+  const uint32_t t = (uint32_t)slot - pg * (uint32_t)p.page_size;
+  if constexpr (MX) soff = times(pg, p.spage_b) + times(t, p.stok_b);
+  return times(pg, p.page_b) + times(t, p.tok_b);
 }
 
 template <typename T>
