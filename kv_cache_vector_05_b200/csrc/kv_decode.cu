@@ -24,16 +24,17 @@
 // 16-byte chunks of tokens 2c, 2c + 1, 2c + 8, 2c + 9 and interleaves them with byte permutes.
 // P goes from the score layout (head pairs) to the operand layout (token pairs) by movmatrix.
 //
-// P enters its product as two 16-bit terms, high and low (16 bits for bf16, 21 for f16): with
-// at most 4 heads the low terms ride in the 4 free columns at no cost, with 5 to 8 they take a
-// second product.
+// P enters its product as 16-bit terms, the first ones rounded towards zero. f16: two terms, 22
+// bits, of p scaled to at most 2^15. bf16: two terms, 16 bits, where out is 16-bit, and a third for
+// fp32. With at most 4 heads the second term rides in the 4 free columns at no cost.
 //
-// MXFP4 records: key codes become f16 operands by the conversion instruction (exact), the block
-// scale multiplies the fp32 sums of its 32 coordinates; the query is scaled by a power of two
-// per head so that its bf16 values fit f16. Value codes become exact bf16 values code 2^e: the
-// f16 code's bits moved to bf16's places are code 2^-112, one multiplication by 2^(112 + e)
-// finishes it (blocks of e > 15 or NaN take two multiplications). A key block of scale 2^-127,
-// the smallest, counts as zero.
+// MXFP4 records: codes become f16 by the conversion instruction (exact). The scale of a key block
+// multiplies the fp32 sums of its 32 coordinates; the query is scaled by a power of two per head
+// so that its bf16 values fit f16. The scale of a value block multiplies its codes in f16, as
+// 2^(e - ref + 13): the sums are kept in units of 2^(ref - 13), ref at least the largest e so far,
+// and codes keep all their bits for e down to ref - 27. Tiles with smaller or NaN blocks take exact
+// bf16 values code 2^e and P in three bf16 terms instead (SLOW). A key block of scale 2^-127, the
+// smallest, counts as zero.
 #include <algorithm>
 #include <atomic>
 
@@ -171,10 +172,12 @@ struct Worker {
   static constexpr int NM = HD / 16;       // 16-coordinate row blocks of the output product
   // P's operand range: bf16 has fp32's exponents; for f16 the largest p is 2^13 to 2^15, so that
   // the smallest step, 2^-24, is at most 2^-37 of it
-  static constexpr bool F16P = !MX && FMT == TQ_KV_F16;
+  static constexpr bool F16P = FMT != TQ_KV_BF16;
   static constexpr float kOff = F16P ? 13.f : 0.f;
   static constexpr float kSlack = F16P ? 2.f : 8.f;
-  static constexpr float kLeast = F16P ? 5.9604644775390625e-8f : 1.17549435e-38f;
+  // ref is set this far above the largest scale seen, and never below kRefLeast, so that p 2^(140 -
+  // ref) of a SLOW tile stays below 2^127
+  static constexpr int kRefSlack = 3, kRefLeast = 32;
 
   const DecArgs& a;
   const int lane, r, c;
@@ -183,6 +186,7 @@ struct Worker {
   float sl[2];
   float acc[NM][4];
   float m[2], l[2];
+  int ref;  // MXFP4: see the top
 
   __device__ Worker(const DecArgs& args, uint32_t ring_base, int ln)
       : a(args), lane(ln), r(ln >> 2), c(ln & 3), ring(ring_base) {}
@@ -319,6 +323,7 @@ struct Worker {
     for (int i = 0; i < NM; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
     m[0] = m[1] = kNegHuge;
     l[0] = l[1] = 0.f;
+    ref = kRefLeast;
   }
 
   // ---- one tile -----------------------------------------------------------------------
@@ -370,7 +375,8 @@ struct Worker {
       out[2 * i + 1] = __byte_perm(xs[i], ys[i], 0x7632);
     }
   }
-  // The same for MXFP4 words with scale factors `f` (bf16 pair): exact bf16 values.
+  // The same for MXFP4 words and factors `f` (a pair): f16 values, or SLOW exact bf16 ones. The f16
+  // code's bits moved to bf16's places are code 2^-112.
   template <bool SLOW>
   static __device__ __forceinline__ void interleave4(uint32_t x, uint32_t y, uint32_t f, uint32_t (&out)[8]) {
     const uint32_t even = (x & 0x0f0f0f0fu) | ((y << 4) & 0xf0f0f0f0u);
@@ -381,22 +387,24 @@ struct Worker {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const uint32_t h = i & 1 ? ho[i >> 1] : he[i >> 1];
-      const uint32_t w = (h & 0x80008000u) | ((h >> 3) & 0x0fff0fffu);  // code 2^-112 as bf16
-      __nv_bfloat162 t = *reinterpret_cast<const __nv_bfloat162*>(&w);
       if constexpr (SLOW) {
-        const uint32_t k = 0x77807780u;  // 2^112
-        t = __hmul2(t, *reinterpret_cast<const __nv_bfloat162*>(&k));
+        const uint32_t w = (h & 0x80008000u) | ((h >> 3) & 0x0fff0fffu), k = 0x77807780u;  // 2^112
+        __nv_bfloat162 t = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&w), *reinterpret_cast<const __nv_bfloat162*>(&k));
+        t = __hmul2(t, *reinterpret_cast<const __nv_bfloat162*>(&f));
+        out[i] = *reinterpret_cast<const uint32_t*>(&t);
+      } else {
+        const __half2 t = __hmul2(*reinterpret_cast<const __half2*>(&h), *reinterpret_cast<const __half2*>(&f));
+        out[i] = *reinterpret_cast<const uint32_t*>(&t);
       }
-      t = __hmul2(t, *reinterpret_cast<const __nv_bfloat162*>(&f));
-      out[i] = *reinterpret_cast<const uint32_t*>(&t);
     }
   }
 
+  // acc += V^T P for the terms b[0], b[1] (SMALL: together in b[0]) and, if `third`, b[2].
   template <bool SLOW>
-  __device__ __forceinline__ void values(uint32_t base, uint32_t bh0, uint32_t bh1, uint32_t bl0, uint32_t bl1) {
+  __device__ __forceinline__ void values(uint32_t base, const uint32_t (&b)[3][2], bool third) {
     const uint32_t v = base + kTile * C::kPitch;
     constexpr int NC = HD / 64;  // 8-coordinate chunks per lane and token
-    using TV = typename std::conditional<MX, __nv_bfloat16, T>::type;
+    using TV = typename std::conditional<MX, typename std::conditional<SLOW, __nv_bfloat16, __half>::type, T>::type;
     uint32_t sc[4][2];
     if constexpr (MX) {
       const uint32_t sv = base + (2 * C::kPitch + C::kScale) * kTile;
@@ -407,6 +415,7 @@ struct Worker {
         sc[i][1] = C::kBlocks == 8 ? lds32(sv + tok * C::kScale + 4) : 0u;
       }
     }
+    const uint32_t bias = (uint32_t)(28 - ref) * (1024u * 0x10001u);  // f16 bits of 2^(byte - ref + 13)
     // chunk n of the tile's tokens: pairs (2c, 2c + 1) in lo, (2c + 8, 2c + 9) in hi
     auto load = [&](int n, uint32_t (&lo)[8], uint32_t (&hi)[8]) {
       if constexpr (!MX) {
@@ -432,16 +441,17 @@ struct Worker {
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           const uint32_t z = __byte_perm(sc[2 * i][n >> 1], sc[2 * i + 1][n >> 1], sel) & 0x00ff00ffu;
-          f[i] = SLOW ? e8m0_bf16(z & 255u) | (e8m0_bf16(z >> 16) << 16)  // 2^e
-                      : (z << 7) + 0x38003800u;                           // 2^(112 + e)
+          f[i] = SLOW ? e8m0_bf16(z & 255u) | (e8m0_bf16(z >> 16) << 16) : z * 1024u + bias;
         }
         interleave4<SLOW>(x[0], x[1], f[0], lo);
         interleave4<SLOW>(x[2], x[3], f[1], hi);
       }
     };
     auto product = [&](float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
-      mma16816<TV>(d, a0, a1, a2, a3, bh0, bh1);
-      if constexpr (!SMALL) mma16816<TV>(d, a0, a1, a2, a3, bl0, bl1);
+      mma16816<TV>(d, a0, a1, a2, a3, b[0][0], b[0][1]);
+      if constexpr (!SMALL) mma16816<TV>(d, a0, a1, a2, a3, b[1][0], b[1][1]);
+      if (SLOW || FMT == TQ_KV_BF16)
+        if (third) mma16816<TV>(d, a0, a1, a2, a3, b[2][0], b[2][1]);
     };
     if constexpr (NC == 1) {
       uint32_t lo[8], hi[8];
@@ -460,9 +470,44 @@ struct Worker {
     }
   }
 
+  // Operand fragments of p's terms in TP. Each is rounded towards zero and the next kept above it
+  // (the last one aside), so that an infinite value meets positive factors and stays infinite.
+  template <typename TP, int TERMS>
+  __device__ __forceinline__ void split(float (&p)[4], uint32_t (&b)[3][2]) const {
+    constexpr float kLeast = std::is_same<TP, __half>::value ? 5.9604644775390625e-8f : 1.17549435e-38f;
+    uint32_t t[3][2];
+#pragma unroll
+    for (int i = 0; i < 3; ++i) {
+      if (i >= TERMS) {
+        t[i][0] = t[i][1] = 0;
+        continue;
+      }
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        t[i][h] = i + 1 < TERMS ? Half2<TP>::pack_rz(p[2 * h], p[2 * h + 1]) : Half2<TP>::pack(p[2 * h], p[2 * h + 1]);
+        if (i + 1 < TERMS) {
+          const float2 g = Half2<TP>::unpack(t[i][h]);
+          p[2 * h] = fmaxf(p[2 * h] - g.x, kLeast);
+          p[2 * h + 1] = fmaxf(p[2 * h + 1] - g.y, kLeast);
+        }
+      }
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      if constexpr (SMALL) {  // columns 4 to 7 hold the same heads' second terms
+        b[0][h] = transpose8x8(c < 2 ? t[0][h] : t[1][h]);
+        b[1][h] = 0;
+        b[2][h] = TERMS == 3 ? transpose8x8(c < 2 ? t[2][h] : 0x00800080u) : 0u;  // kLeast: as above
+      } else {
+        b[0][h] = transpose8x8(t[0][h]);
+        b[1][h] = transpose8x8(t[1][h]);
+        b[2][h] = TERMS == 3 ? transpose8x8(t[2][h]) : 0u;
+      }
+    }
+  }
+
   template <bool SLOW>
   __device__ __forceinline__ void tile(const Cursor& u, uint32_t base) {
-    using TP = typename std::conditional<F16P, __half, __nv_bfloat16>::type;
     float s[4] = {0.f, 0.f, 0.f, 0.f};
     scores<SLOW>(base, s);
     s[0] *= sl[0], s[1] *= sl[1], s[2] *= sl[0], s[3] *= sl[1];
@@ -491,30 +536,68 @@ struct Worker {
     p[0] = ex2(s[0] - m[0]), p[1] = ex2(s[1] - m[1]), p[2] = ex2(s[2] - m[0]), p[3] = ex2(s[3] - m[1]);
     l[0] += p[0] + p[2];
     l[1] += p[1] + p[3];
-    // The high term is rounded towards zero and the low one kept above it, so that an infinite
-    // value meets two positive factors and stays infinite.
-    uint32_t h0 = Half2<TP>::pack_rz(p[0], p[1]), h1 = Half2<TP>::pack_rz(p[2], p[3]);
-    const float2 g0 = Half2<TP>::unpack(h0), g1 = Half2<TP>::unpack(h1);
-    const uint32_t l0 = Half2<TP>::pack(fmaxf(p[0] - g0.x, kLeast), fmaxf(p[1] - g0.y, kLeast));
-    const uint32_t l1 = Half2<TP>::pack(fmaxf(p[2] - g1.x, kLeast), fmaxf(p[3] - g1.y, kLeast));
-    if constexpr (SMALL) {  // columns 4 to 7 hold the same heads' low terms
-      h0 = c < 2 ? h0 : l0;
-      h1 = c < 2 ? h1 : l1;
-      values<SLOW>(base, transpose8x8(h0), transpose8x8(h1), 0, 0);
+    uint32_t b[3][2];
+    if constexpr (SLOW) {  // values in units of 1, sums in units of 2^(ref - 127 - 13)
+      const float f = __uint_as_float((uint32_t)(127 + 140 - ref) << 23);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) p[i] *= f;
+      split<__nv_bfloat16, 3>(p, b);
+      values<true>(base, b, true);
+    } else if constexpr (F16P) {
+      split<__half, 2>(p, b);
+      values<false>(base, b, false);
+    } else if (a.out_f32) {
+      split<__nv_bfloat16, 3>(p, b);
+      values<false>(base, b, true);
     } else {
-      values<SLOW>(base, transpose8x8(h0), transpose8x8(h1), transpose8x8(l0), transpose8x8(l1));
+      split<__nv_bfloat16, 2>(p, b);
+      values<false>(base, b, false);
     }
   }
 
   __device__ __forceinline__ void step(const Cursor& u, int st) {
     const uint32_t base = ring + st * C::kStageBytes;
     if constexpr (MX) {
-      // lane i's scale word of the tile: 16 key rows, then 16 value rows
-      uint32_t w = lds32(base + 2 * kTile * C::kPitch + lane * C::kScale);
-      uint32_t w2 = C::kBlocks == 8 ? lds32(base + 2 * kTile * C::kPitch + lane * C::kScale + 4) : 0u;
-      w = __vmaxu4(w, w2);
-      const uint32_t limit = lane < 16 ? 0xfefefefeu : 0x8e8e8e8eu;  // keys: not NaN; values: e <= 15
-      if (__any_sync(kFull, __vmaxu4(w, limit) != limit)) {
+      // lane i's scale words of the tile: 16 key rows, then 16 value rows
+      const uint32_t at = base + 2 * kTile * C::kPitch + lane * C::kScale;
+      uint32_t w[2] = {lds32(at), C::kBlocks == 8 ? lds32(at + 4) : 0u};
+      const int t = (u.e.lo / kTile + u.tile) * kTile, row = t + (lane & 15);
+      const bool is_v = lane >= 16, valid = row >= u.e.lo && row < u.e.len;
+      bool nan = false, over = false, under = false;
+      const uint32_t ref4 = (uint32_t)min(ref, 254) * 0x01010101u;
+#pragma unroll
+      for (int i = 0; i < (C::kBlocks == 8 ? 2 : 1); ++i) {
+        const uint32_t n = __vcmpeq4(w[i], 0xffffffffu);
+        nan |= n != 0;
+        w[i] &= ~n;
+        over |= is_v && __vmaxu4(w[i], ref4) != ref4;
+      }
+      if (__any_sync(kFull, over)) {
+        uint32_t x = __vmaxu4(w[0], w[1]);
+        x = max(max(x & 255u, x >> 8 & 255u), max(x >> 16 & 255u, x >> 24));
+        const int top = (int)__reduce_max_sync(kFull, is_v ? x : 0u) + kRefSlack;  // above ref
+        // 2^(ref - top) in two steps: it may lie below fp32's range
+        const int d0 = (ref - top) / 2, d1 = ref - top - d0;
+        const float f0 = __uint_as_float((uint32_t)(127 + d0) << 23), f1 = __uint_as_float((uint32_t)(127 + d1) << 23);
+#pragma unroll
+        for (int i = 0; i < NM; ++i)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) acc[i][j] = acc[i][j] * f0 * f1;
+        ref = top;
+      }
+      const uint32_t low4 = (uint32_t)max(ref - 27, 0) * 0x01010101u;
+      const uint32_t used = C::kBlocks == 2 ? 0x0000ffffu : 0xffffffffu;  // bytes of a word that are scales
+#pragma unroll
+      for (int i = 0; i < (C::kBlocks == 8 ? 2 : 1); ++i) under |= is_v && valid && ((__vminu4(w[i], low4) ^ low4) & used);
+      if (t < u.e.lo || t + kTile > u.e.len) {  // rows outside the sequence: any factor in range
+        const uint32_t any4 = (uint32_t)min(max(ref - 27, 0), 254) * 0x01010101u;
+        if (is_v && !valid) {
+          asm volatile("st.shared.b32 [%0], %1;" ::"r"(at), "r"(any4) : "memory");
+          if (C::kBlocks == 8) asm volatile("st.shared.b32 [%0], %1;" ::"r"(at + 4), "r"(any4) : "memory");
+        }
+        __syncwarp();
+      }
+      if (__any_sync(kFull, nan || under)) {
         tile<true>(u, base);
         return;
       }
@@ -526,6 +609,16 @@ struct Worker {
 
   // Sum the lanes' shares: l over the tokens, and the low terms' columns.
   __device__ __forceinline__ void finish() {
+    if constexpr (MX) {  // out of units of 2^(ref - 127 - 13) and of p's 2^kOff
+      const int x = ref - 140 - (int)kOff, d0 = x / 2, d1 = x - d0;
+      const float f0 = __uint_as_float((uint32_t)(127 + d0) << 23), f1 = __uint_as_float((uint32_t)(127 + d1) << 23);
+#pragma unroll
+      for (int i = 0; i < NM; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[i][j] = acc[i][j] * f0 * f1;
+#pragma unroll
+      for (int j = 0; j < 2; ++j) l[j] *= 1.f / (1 << (int)kOff), m[j] += kOff;
+    }
 #pragma unroll
     for (int j = 0; j < 2; ++j)
 #pragma unroll

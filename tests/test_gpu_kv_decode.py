@@ -219,7 +219,10 @@ def test_decode_mxfp4_full_scale_range():
     cache[0][int(table[1, 2]), 1] = 0
     cache[2][int(table[1, 2]), 1, 0, 2] = 255
     out2, lse2 = T.tq_decode_kv_pages(ctx, q, T.KVPages(*cache), hkv, up(table), 80, seq_lens=up(lens.astype(np.int32)))
-    assert torch.isnan(out2[0, :, 32:64]).all() and torch.equal(out2[0, :, :32], out[0, :, :32])
+    assert torch.isnan(out2[0, :, 32:64]).all()
+    # the other blocks of that row pass through the tile's other products: each is off by at most the
+    # 2^-17 of P's terms, twice max|v| = 6 x 2^(2 - 127)
+    assert (out2[0, :, :32] - out[0, :, :32]).abs().max() <= 2 * 2 * 2.0 ** -17 * 6 * 2.0 ** -125
     assert torch.isnan(out2[1]).all() and torch.isnan(lse2[1]).all()
     assert torch.equal(out2[2:], out[2:]) and torch.equal(lse2[2:], lse[2:])
 
