@@ -47,8 +47,7 @@ namespace {
 
 using sm100::smem_u32;
 
-constexpr int kTile = 16;          // tokens per tile (one MMA row block)
-constexpr int kMinTiles = 2;       // fewest tiles a warp is given before CTAs are left out
+constexpr int kRows = 16;          // tokens of one MMA row block; pages of whole blocks are looked up per block
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kNegHuge = -1.7e38f;  // maximum of no logits: finite, so that -inf - m is -inf
 
@@ -75,12 +74,17 @@ struct DecArgs {
 template <int FMT, int HD>
 struct Config {
   static constexpr bool MX = FMT == TQ_KV_MXFP4;
+  // Tokens per tile. MXFP4 takes two row blocks at a time: its per-tile work (copies, looking over
+  // the scales, the maximum) is a third of a tile's and every lane has a key and a value row's
+  // scales to look at.
+  static constexpr int kTile = MX ? 32 : 16, kBlocksT = kTile / kRows;
   static constexpr int kWarps = MX ? (HD == 256 ? 8 : 16) : (HD == 256 ? 4 : 8);
   static constexpr int kPitch = MX ? HD / 2 + 16 : HD * 2;       // bytes between records of a stage
   static constexpr int kBlocks = HD / 32;                        // scale bytes of an MXFP4 record
   static constexpr int kScale = MX ? (kBlocks < 4 ? 4 : kBlocks) : 0;  // their room in a stage
   static constexpr int kStageBytes = 2 * kTile * (kPitch + kScale);
-  static constexpr int kStages = MX ? 5 : (HD == 64 ? 6 : 3);
+  static constexpr int kStages = MX ? (HD == 64 ? 4 : 2) : (HD == 64 ? 6 : 3);
+  static constexpr int kMinTiles = 32 / kTile;  // fewest tiles a warp is given before CTAs are left out
   static constexpr int kRing = kStages * kStageBytes;
   static constexpr int kSmem = kWarps * kRing;
 };
@@ -145,6 +149,7 @@ __device__ __forceinline__ int chunk_swizzle(int row) { return (((row >> 1) & 3)
 struct Extent {
   int len, lo, nt;
 };
+template <int kTile>
 __device__ __forceinline__ Extent extent(const DecArgs& a, int b) {
   int64_t n = a.lens ? (int64_t)__ldg(a.lens + b) : a.max_len;
   n = n < 0 ? 0 : n > a.max_len ? a.max_len : n;
@@ -159,15 +164,15 @@ __device__ __forceinline__ Extent extent(const DecArgs& a, int b) {
 struct Cursor {
   Extent e;
   int b, uk, tile;
-  int blk;      // block-table index of the tile's first token
-  int off;      // its place in the page (pages of whole tiles)
-  int page;     // its entry of the block table, loaded ahead of its use and checked then
+  int off[2];   // pages of whole row blocks: place of each block's first token in its page,
+  int page[2];  // and the page's entry of the block table, loaded ahead of its use and checked then
 };
 
 template <typename T, int FMT, int HD, bool SMALL, bool WHOLE>
 struct Worker {
   using C = Config<FMT, HD>;
   static constexpr bool MX = C::MX;
+  static constexpr int kTile = C::kTile, kBlocksT = C::kBlocksT;
   static constexpr int NK = HD / 32;       // 32-coordinate steps of the score product
   static constexpr int NM = HD / 16;       // 16-coordinate row blocks of the output product
   // P's operand range: bf16 has fp32's exponents; for f16 the largest p is 2^13 to 2^15, so that
@@ -203,32 +208,29 @@ struct Worker {
     return 0;
   }
 
-  // Enter unit (b, uk) at `tile`; the page of the tile is looked up at once for WHOLE pages.
+  // Look up the pages of the cursor's tile (a row block past the sequence's end stands in the
+  // last one's place: none of its tokens is read).
   __device__ __forceinline__ void place(Cursor& u) const {
     if constexpr (WHOLE) {
-      const int t = (u.e.lo / kTile + u.tile) * kTile;
-      u.blk = t / (int)a.pg.page_size;
-      u.off = t - u.blk * (int)a.pg.page_size;
-      u.page = page_of(u, u.blk);
+#pragma unroll
+      for (int h = 0; h < kBlocksT; ++h) {
+        int t = (u.e.lo / kTile + u.tile) * kTile + h * kRows;
+        if (h && t >= u.e.len) t -= kRows;
+        const int blk = a.pg.page_shift >= 0 ? t >> a.pg.page_shift : t / (int)a.pg.page_size;
+        u.off[h] = t - blk * (int)a.pg.page_size;
+        u.page[h] = page_of(u, blk);
+      }
     }
   }
   __device__ __forceinline__ void advance(Cursor& u) const {
-    if (++u.tile < u.e.nt) {
-      if constexpr (WHOLE) {
-        u.off += kTile;
-        if (u.off == (int)a.pg.page_size) {
-          u.off = 0;
-          u.page = page_of(u, ++u.blk);
-        }
+    if (++u.tile == u.e.nt) {
+      u.tile = 0;
+      if (++u.uk == a.pg.hkv * a.HB) {
+        u.uk = 0;
+        do {
+          u.e = extent<kTile>(a, ++u.b);
+        } while (u.e.nt == 0);
       }
-      return;
-    }
-    u.tile = 0;
-    if (++u.uk == a.pg.hkv * a.HB) {
-      u.uk = 0;
-      do {
-        u.e = extent(a, ++u.b);
-      } while (u.e.nt == 0);
     }
     place(u);
   }
@@ -240,44 +242,47 @@ struct Worker {
     const uint32_t base = ring + st * C::kStageBytes;
     const int t = (u.e.lo / kTile + u.tile) * kTile;
     const int kvh = u.uk / a.HB;
-    int64_t off0 = 0, soff0 = 0;
-    if constexpr (WHOLE) {
-      const int64_t pg = checked(u.page);
-      off0 = pg * a.pg.page_b + (int64_t)u.off * a.pg.tok_b + (int64_t)kvh * a.pg.head_b;
-      if constexpr (MX) soff0 = pg * a.pg.spage_b + (int64_t)u.off * a.pg.stok_b + (int64_t)kvh * a.pg.shead_b;
-    } else {
-      // each of 16 lanes looks up one token's page; the others receive it by shuffles
-      int tok = t + (lane & 15);
-      tok = tok < u.e.lo ? u.e.lo : tok >= u.e.len ? u.e.len - 1 : tok;
-      const int blk = tok / (int)a.pg.page_size, o = tok - blk * (int)a.pg.page_size;
-      const int64_t pg = checked(page_of(u, blk));
-      off0 = pg * a.pg.page_b + (int64_t)o * a.pg.tok_b + (int64_t)kvh * a.pg.head_b;
-      if constexpr (MX) soff0 = pg * a.pg.spage_b + (int64_t)o * a.pg.stok_b + (int64_t)kvh * a.pg.shead_b;
-    }
     constexpr int CPR = MX ? HD / 32 : HD / 8;  // 16-byte chunks per record
     constexpr int RP = 32 / CPR;                // records per instruction
     const int row0 = lane / CPR, ch = lane % CPR;
 #pragma unroll
-    for (int j = 0; j < (kTile + RP - 1) / RP; ++j) {
-      const int row = row0 + j * RP;
-      if (RP > kTile && row >= kTile) break;
-      const bool ok = t + row >= u.e.lo && t + row < u.e.len;
-      const int64_t off = (WHOLE ? off0 + (int64_t)row * a.pg.tok_b : __shfl_sync(kFull, off0, row)) + ch * 16;
-      const uint32_t dst = base + row * C::kPitch + (MX ? ch : (ch ^ chunk_swizzle(row))) * 16;
-      cp_async<16>(dst, a.pg.k + off, ok);
-      cp_async<16>(dst + kTile * C::kPitch, a.pg.v + off, ok);
-    }
-    if constexpr (MX) {
-      const int row = lane & 15;
-      const bool ok = t + row >= u.e.lo && t + row < u.e.len;
-      const int64_t off = WHOLE ? soff0 + (int64_t)row * a.pg.stok_b : soff0;
-      const uint8_t* src = (lane < 16 ? a.pg.ks : a.pg.vs) + off;
-      const uint32_t dst = base + 2 * kTile * C::kPitch + lane * C::kScale;
-      if constexpr (C::kBlocks == 2) {  // below cp.async's sizes
-        const uint32_t w = ok ? *reinterpret_cast<const uint16_t*>(src) : 0u;
-        asm volatile("st.shared.b32 [%0], %1;" ::"r"(dst), "r"(w) : "memory");
+    for (int h = 0; h < kBlocksT; ++h) {
+      int64_t off0 = 0, soff0 = 0;
+      if constexpr (WHOLE) {
+        const uint32_t pg = (uint32_t)checked(u.page[h]);
+        off0 = times(pg, a.pg.page_b) + times(u.off[h], a.pg.tok_b) + times(kvh, a.pg.head_b);
+        if constexpr (MX) soff0 = times(pg, a.pg.spage_b) + times(u.off[h], a.pg.stok_b) + times(kvh, a.pg.shead_b);
       } else {
-        cp_async<C::kBlocks>(dst, src, ok);
+        // each of 16 lanes looks up one token's page; the others receive it by shuffles
+        int tok = t + h * kRows + (lane & 15);
+        tok = tok < u.e.lo ? u.e.lo : tok >= u.e.len ? u.e.len - 1 : tok;
+        const int blk = tok / (int)a.pg.page_size, o = tok - blk * (int)a.pg.page_size;
+        const uint32_t pg = (uint32_t)checked(page_of(u, blk));
+        off0 = times(pg, a.pg.page_b) + times(o, a.pg.tok_b) + times(kvh, a.pg.head_b);
+        if constexpr (MX) soff0 = times(pg, a.pg.spage_b) + times(o, a.pg.stok_b) + times(kvh, a.pg.shead_b);
+      }
+      const int64_t mine = off0 + (WHOLE ? times(row0, a.pg.tok_b) : 0) + ch * 16;
+#pragma unroll
+      for (int j = 0; j < kRows / RP; ++j) {
+        const int row = h * kRows + row0 + j * RP;
+        const bool ok = t + row >= u.e.lo && t + row < u.e.len;
+        const int64_t off = WHOLE ? mine + j * RP * a.pg.tok_b : __shfl_sync(kFull, off0, row0 + j * RP) + ch * 16;
+        const uint32_t dst = base + row * C::kPitch + (MX ? ch : (ch ^ chunk_swizzle(row))) * 16;
+        cp_async<16>(dst, a.pg.k + off, ok);
+        cp_async<16>(dst + kTile * C::kPitch, a.pg.v + off, ok);
+      }
+      if constexpr (MX) {  // scales: lanes 0-15 key rows, 16-31 value rows of the block
+        const int row = h * kRows + (lane & 15);
+        const bool ok = t + row >= u.e.lo && t + row < u.e.len;
+        const int64_t off = WHOLE ? soff0 + times(lane & 15, a.pg.stok_b) : soff0;
+        const uint8_t* src = (lane < 16 ? a.pg.ks : a.pg.vs) + off;
+        const uint32_t dst = base + 2 * kTile * C::kPitch + ((lane < 16 ? 0 : kTile) + row) * C::kScale;
+        if constexpr (C::kBlocks == 2) {  // below cp.async's sizes
+          const uint32_t w = ok ? *reinterpret_cast<const uint16_t*>(src) : 0u;
+          asm volatile("st.shared.b32 [%0], %1;" ::"r"(dst), "r"(w) : "memory");
+        } else {
+          cp_async<C::kBlocks>(dst, src, ok);
+        }
       }
     }
   }
@@ -330,10 +335,10 @@ struct Worker {
 
   // SLOW: some scale byte of the tile needs the full range (see the top comment).
   template <bool SLOW>
-  __device__ __forceinline__ void scores(uint32_t base, float (&s)[4]) const {
+  __device__ __forceinline__ void scores(uint32_t base, int h, float (&s)[4]) const {
     if constexpr (!MX) {
       float s2[4] = {0.f, 0.f, 0.f, 0.f};
-      const uint32_t row = base + r * C::kPitch;
+      const uint32_t row = base + (h * kRows + r) * C::kPitch;
       const int sw = chunk_swizzle(r);
 #pragma unroll
       for (int i = 0; i < NK; ++i) {
@@ -345,8 +350,14 @@ struct Worker {
 #pragma unroll
       for (int i = 0; i < 4; ++i) s[i] += s2[i];
     } else {
-      const uint32_t row = base + r * C::kPitch + c * 4;
-      const uint32_t srow = base + 2 * kTile * C::kPitch + r * C::kScale;
+      const uint32_t row = base + (h * kRows + r) * C::kPitch + c * 4;
+      const uint32_t srow = base + 2 * kTile * C::kPitch + (h * kRows + r) * C::kScale;
+      uint32_t w[2][2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        w[i][0] = lds32(srow + i * 8 * C::kScale);
+        w[i][1] = C::kBlocks == 8 ? lds32(srow + i * 8 * C::kScale + 4) : 0u;
+      }
 #pragma unroll
       for (int i = 0; i < NK; ++i) {
         uint32_t x[4], y[4];
@@ -355,9 +366,14 @@ struct Worker {
         float g[4] = {0.f, 0.f, 0.f, 0.f};
         mma16816<__half>(g, x[0], y[0], x[1], y[1], q[i][0], q[i][1]);
         mma16816<__half>(g, x[2], y[2], x[3], y[3], q[i][2], q[i][3]);
-        const uint32_t w0 = lds32(srow + (i & ~3)), w1 = lds32(srow + 8 * C::kScale + (i & ~3));
-        const uint32_t b0 = (w0 >> (8 * (i & 3))) & 255u, b1 = (w1 >> (8 * (i & 3))) & 255u;
-        const float f0 = SLOW ? e8m0(b0) : __uint_as_float(b0 << 23), f1 = SLOW ? e8m0(b1) : __uint_as_float(b1 << 23);
+        float f[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const uint32_t x = w[e][i >> 2];
+          if (SLOW) f[e] = e8m0((x >> (8 * (i & 3))) & 255u);
+          else f[e] = __uint_as_float((i & 3) == 3 ? (x >> 1) & 0x7f800000u : (x << (23 - 8 * (i & 3))) & 0x7f800000u);
+        }
+        const float f0 = f[0], f1 = f[1];
         s[0] = fmaf(g[0], f0, s[0]);
         s[1] = fmaf(g[1], f0, s[1]);
         s[2] = fmaf(g[2], f1, s[2]);
@@ -401,13 +417,13 @@ struct Worker {
 
   // acc += V^T P for the terms b[0], b[1] (SMALL: together in b[0]) and, if `third`, b[2].
   template <bool SLOW>
-  __device__ __forceinline__ void values(uint32_t base, const uint32_t (&b)[3][2], bool third) {
-    const uint32_t v = base + kTile * C::kPitch;
+  __device__ __forceinline__ void values(uint32_t base, int h, const uint32_t (&b)[3][2], bool third) {
+    const uint32_t v = base + (kTile + h * kRows) * C::kPitch;
     constexpr int NC = HD / 64;  // 8-coordinate chunks per lane and token
     using TV = typename std::conditional<MX, typename std::conditional<SLOW, __nv_bfloat16, __half>::type, T>::type;
     uint32_t sc[4][2];
     if constexpr (MX) {
-      const uint32_t sv = base + (2 * C::kPitch + C::kScale) * kTile;
+      const uint32_t sv = base + (2 * C::kPitch + C::kScale) * kTile + h * kRows * C::kScale;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int tok = 2 * c + (i & 1) + (i >> 1) * 8;
@@ -508,16 +524,22 @@ struct Worker {
 
   template <bool SLOW>
   __device__ __forceinline__ void tile(const Cursor& u, uint32_t base) {
-    float s[4] = {0.f, 0.f, 0.f, 0.f};
-    scores<SLOW>(base, s);
-    s[0] *= sl[0], s[1] *= sl[1], s[2] *= sl[0], s[3] *= sl[1];
+    float s[kBlocksT][4];
     const int t = (u.e.lo / kTile + u.tile) * kTile;
-    if (t < u.e.lo || t + kTile > u.e.len) {
-      if (t + r < u.e.lo || t + r >= u.e.len) s[0] = s[1] = -INFINITY;
-      if (t + r + 8 < u.e.lo || t + r + 8 >= u.e.len) s[2] = s[3] = -INFINITY;
+    float x0 = -INFINITY, x1 = -INFINITY;
+#pragma unroll
+    for (int h = 0; h < kBlocksT; ++h) {
+      s[h][0] = s[h][1] = s[h][2] = s[h][3] = 0.f;
+      scores<SLOW>(base, h, s[h]);
+      s[h][0] *= sl[0], s[h][1] *= sl[1], s[h][2] *= sl[0], s[h][3] *= sl[1];
+      if (t < u.e.lo || t + kTile > u.e.len) {
+        const int a0 = t + h * kRows + r;
+        if (a0 < u.e.lo || a0 >= u.e.len) s[h][0] = s[h][1] = -INFINITY;
+        if (a0 + 8 < u.e.lo || a0 + 8 >= u.e.len) s[h][2] = s[h][3] = -INFINITY;
+      }
+      x0 = fmaxf(x0, fmaxf(s[h][0], s[h][2])), x1 = fmaxf(x1, fmaxf(s[h][1], s[h][3]));
     }
     // m is moved only when a logit passes it by kSlack (then p would leave its range)
-    const float x0 = fmaxf(s[0], s[2]), x1 = fmaxf(s[1], s[3]);
     if (__any_sync(kFull, x0 > m[0] + (kOff + kSlack) || x1 > m[1] + (kOff + kSlack))) {
       float n[2] = {x0, x1};
 #pragma unroll
@@ -532,50 +554,55 @@ struct Worker {
         for (int i = 0; i < NM; ++i) acc[i][j] *= f, acc[i][2 + j] *= f;
       }
     }
-    float p[4];
-    p[0] = ex2(s[0] - m[0]), p[1] = ex2(s[1] - m[1]), p[2] = ex2(s[2] - m[0]), p[3] = ex2(s[3] - m[1]);
-    l[0] += p[0] + p[2];
-    l[1] += p[1] + p[3];
-    uint32_t b[3][2];
-    if constexpr (SLOW) {  // values in units of 1, sums in units of 2^(ref - 127 - 13)
-      const float f = __uint_as_float((uint32_t)(127 + 140 - ref) << 23);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) p[i] *= f;
-      split<__nv_bfloat16, 3>(p, b);
-      values<true>(base, b, true);
-    } else if constexpr (F16P) {
-      split<__half, 2>(p, b);
-      values<false>(base, b, false);
-    } else if (a.out_f32) {
-      split<__nv_bfloat16, 3>(p, b);
-      values<false>(base, b, true);
-    } else {
-      split<__nv_bfloat16, 2>(p, b);
-      values<false>(base, b, false);
+    for (int h = 0; h < kBlocksT; ++h) {
+      float p[4];
+      p[0] = ex2(s[h][0] - m[0]), p[1] = ex2(s[h][1] - m[1]), p[2] = ex2(s[h][2] - m[0]), p[3] = ex2(s[h][3] - m[1]);
+      l[0] += p[0] + p[2];
+      l[1] += p[1] + p[3];
+      uint32_t b[3][2];
+      if constexpr (SLOW) {  // values in units of 1, sums in units of 2^(ref - 127 - 13)
+        const float f = __uint_as_float((uint32_t)(127 + 140 - ref) << 23);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) p[i] *= f;
+        split<__nv_bfloat16, 3>(p, b);
+        values<true>(base, h, b, true);
+      } else if constexpr (F16P) {
+        split<__half, 2>(p, b);
+        values<false>(base, h, b, false);
+      } else if (a.out_f32) {
+        split<__nv_bfloat16, 3>(p, b);
+        values<false>(base, h, b, true);
+      } else {
+        split<__nv_bfloat16, 2>(p, b);
+        values<false>(base, h, b, false);
+      }
     }
   }
 
   __device__ __forceinline__ void step(const Cursor& u, int st) {
     const uint32_t base = ring + st * C::kStageBytes;
     if constexpr (MX) {
-      // lane i's scale words of the tile: 16 key rows, then 16 value rows
-      const uint32_t at = base + 2 * kTile * C::kPitch + lane * C::kScale;
-      uint32_t w[2] = {lds32(at), C::kBlocks == 8 ? lds32(at + 4) : 0u};
-      const int t = (u.e.lo / kTile + u.tile) * kTile, row = t + (lane & 15);
-      const bool is_v = lane >= 16, valid = row >= u.e.lo && row < u.e.len;
+      // lane i's scale words: key row i and value row i of the tile
+      constexpr int NW = C::kBlocks == 8 ? 2 : 1;
+      const uint32_t ak = base + 2 * kTile * C::kPitch + lane * C::kScale, av = ak + kTile * C::kScale;
+      const int t = (u.e.lo / kTile + u.tile) * kTile;
+      const bool valid = t + lane >= u.e.lo && t + lane < u.e.len;
       bool nan = false, over = false, under = false;
       const uint32_t ref4 = (uint32_t)min(ref, 254) * 0x01010101u;
+      uint32_t w[NW];
 #pragma unroll
-      for (int i = 0; i < (C::kBlocks == 8 ? 2 : 1); ++i) {
+      for (int i = 0; i < NW; ++i) {
+        w[i] = lds32(av + 4 * i);
         const uint32_t n = __vcmpeq4(w[i], 0xffffffffu);
-        nan |= n != 0;
+        nan |= n != 0 || __vcmpeq4(lds32(ak + 4 * i), 0xffffffffu) != 0;
         w[i] &= ~n;
-        over |= is_v && __vmaxu4(w[i], ref4) != ref4;
+        over |= __vmaxu4(w[i], ref4) != ref4;
       }
       if (__any_sync(kFull, over)) {
-        uint32_t x = __vmaxu4(w[0], w[1]);
-        x = max(max(x & 255u, x >> 8 & 255u), max(x >> 16 & 255u, x >> 24));
-        const int top = (int)__reduce_max_sync(kFull, is_v ? x : 0u) + kRefSlack;  // above ref
+        const uint32_t x = __vmaxu4(w[0], w[NW - 1]);
+        const int top = (int)__reduce_max_sync(kFull, max(max(x & 255u, x >> 8 & 255u), max(x >> 16 & 255u, x >> 24))) +
+                        kRefSlack;
         // 2^(ref - top) in two steps: it may lie below fp32's range
         const int d0 = (ref - top) / 2, d1 = ref - top - d0;
         const float f0 = __uint_as_float((uint32_t)(127 + d0) << 23), f1 = __uint_as_float((uint32_t)(127 + d1) << 23);
@@ -588,13 +615,12 @@ struct Worker {
       const uint32_t low4 = (uint32_t)max(ref - 27, 0) * 0x01010101u;
       const uint32_t used = C::kBlocks == 2 ? 0x0000ffffu : 0xffffffffu;  // bytes of a word that are scales
 #pragma unroll
-      for (int i = 0; i < (C::kBlocks == 8 ? 2 : 1); ++i) under |= is_v && valid && ((__vminu4(w[i], low4) ^ low4) & used);
+      for (int i = 0; i < NW; ++i) under |= valid && ((__vminu4(w[i], low4) ^ low4) & used);
       if (t < u.e.lo || t + kTile > u.e.len) {  // rows outside the sequence: any factor in range
         const uint32_t any4 = (uint32_t)min(max(ref - 27, 0), 254) * 0x01010101u;
-        if (is_v && !valid) {
-          asm volatile("st.shared.b32 [%0], %1;" ::"r"(at), "r"(any4) : "memory");
-          if (C::kBlocks == 8) asm volatile("st.shared.b32 [%0], %1;" ::"r"(at + 4), "r"(any4) : "memory");
-        }
+#pragma unroll
+        for (int i = 0; i < NW; ++i)
+          if (!valid) asm volatile("st.shared.b32 [%0], %1;" ::"r"(av + 4 * i), "r"(any4) : "memory");
         __syncwarp();
       }
       if (__any_sync(kFull, nan || under)) {
@@ -731,12 +757,12 @@ __global__ void __launch_bounds__(Config<FMT, HD>::kWarps * 32, 1) kv_decode_ker
   int n;
   auto divide = [&](int64_t all) {
     total = all * upb;
-    const int64_t want = (total + W * kMinTiles - 1) / (W * kMinTiles);
+    const int64_t want = (total + W * C::kMinTiles - 1) / (W * C::kMinTiles);
     n = (int)(want < gridDim.x ? want : gridDim.x);
     cta0 = n ? scaled(total, k, n) : 0;
   };
   if (a.batch <= NT) {  // one scan gives both
-    const int64_t mine = tid < a.batch ? extent(a, tid).nt : 0;
+    const int64_t mine = tid < a.batch ? extent<C::kTile>(a, tid).nt : 0;
     const int64_t incl = warp_incl_scan(mine, lane);
     if (lane == 31) s_scan[w] = incl;
     __syncthreads();
@@ -753,7 +779,7 @@ __global__ void __launch_bounds__(Config<FMT, HD>::kWarps * 32, 1) kv_decode_ker
     }
   } else {
     int64_t sum = 0;
-    for (int b = tid; b < a.batch; b += NT) sum += extent(a, b).nt;
+    for (int b = tid; b < a.batch; b += NT) sum += extent<C::kTile>(a, b).nt;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kFull, sum, o);
     if (lane == 0) s_scan[w] = sum;
@@ -765,7 +791,7 @@ __global__ void __launch_bounds__(Config<FMT, HD>::kWarps * 32, 1) kv_decode_ker
     int64_t base = 0;
     for (int64_t b0 = 0; k < n && base <= cta0; b0 += NT) {
       const int b = (int)b0 + tid;
-      const int64_t mine = b < a.batch ? (int64_t)extent(a, b).nt * upb : 0;
+      const int64_t mine = b < a.batch ? (int64_t)extent<C::kTile>(a, b).nt * upb : 0;
       const int64_t incl = warp_incl_scan(mine, lane);
       __syncthreads();  // s_scan has been read
       if (lane == 31) s_scan[w] = incl;
@@ -795,10 +821,10 @@ __global__ void __launch_bounds__(Config<FMT, HD>::kWarps * 32, 1) kv_decode_ker
   if (r0 < r1) {
     int64_t start = s_start;
     cur.b = s_b;
-    cur.e = extent(a, cur.b);
+    cur.e = extent<C::kTile>(a, cur.b);
     while (r0 >= start + (int64_t)cur.e.nt * upb) {
       start += (int64_t)cur.e.nt * upb;
-      cur.e = extent(a, ++cur.b);
+      cur.e = extent<C::kTile>(a, ++cur.b);
     }
     cur.uk = (int)quotient(r0 - start, cur.e.nt);
     cur.tile = (int)(r0 - start - (int64_t)cur.uk * cur.e.nt);
@@ -848,7 +874,7 @@ __global__ void __launch_bounds__(Config<FMT, HD>::kWarps * 32, 1) kv_decode_ker
           if (++cur.uk == upb) {
             cur.uk = 0;
             do {
-              cur.e = extent(a, ++cur.b);
+              cur.e = extent<C::kTile>(a, ++cur.b);
             } while (cur.e.nt == 0);
           }
           seg_from = 0;
@@ -927,7 +953,7 @@ __global__ void __launch_bounds__(Config<FMT, HD>::kWarps * 32, 1) kv_decode_ker
 
   // sequences without tokens: zero rows
   for (int b = k; b < a.batch; b += gridDim.x) {
-    if (extent(a, b).nt) continue;
+    if (extent<C::kTile>(a, b).nt) continue;
     for (int i = tid; i < a.hq * (HD / 4); i += NT)
       store4(a, std::is_same<T, __half>::value, (int64_t)b * a.hq * HD + i * 4, make_float4(0.f, 0.f, 0.f, 0.f));
     if (a.lse)
@@ -1024,7 +1050,7 @@ cudaError_t run(const DecArgs& a, int device, int ctas, cudaStream_t st) {
 
 template <typename T, int FMT, int HD>
 cudaError_t pick(const DecArgs& a, int device, int ctas, cudaStream_t st) {
-  const bool whole = a.pg.page_size % kTile == 0;
+  const bool whole = a.pg.page_size % kRows == 0;
   if (a.GB <= 4) return whole ? run<T, FMT, HD, true, true>(a, device, ctas, st) : run<T, FMT, HD, true, false>(a, device, ctas, st);
   return whole ? run<T, FMT, HD, false, true>(a, device, ctas, st) : run<T, FMT, HD, false, false>(a, device, ctas, st);
 }
