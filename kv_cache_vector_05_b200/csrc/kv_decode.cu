@@ -108,6 +108,14 @@ __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+// d = A B for f16 operands (no accumulator to clear).
+__device__ __forceinline__ void mma16816_new(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                             uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
+
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
   uint32_t y;
   asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
@@ -160,10 +168,11 @@ __device__ __forceinline__ Extent extent(const DecArgs& a, int b) {
   return e;
 }
 
-// A position in the work: tile `tile` of unit `uk` of sequence `b`, and the page of its block.
+// A position in the work: tile `tile` of query-head block `hb` of KV head `kvh` of sequence `b`,
+// and the pages of its row blocks.
 struct Cursor {
   Extent e;
-  int b, uk, tile;
+  int b, kvh, hb, tile;
   int off[2];   // pages of whole row blocks: place of each block's first token in its page,
   int page[2];  // and the page's entry of the block table, loaded ahead of its use and checked then
 };
@@ -199,7 +208,7 @@ struct Worker {
   // ---- loads ------------------------------------------------------------------------
 
   __device__ __forceinline__ int page_of(const Cursor& u, int blk) const {
-    const int64_t row = a.pg.per_head ? (int64_t)u.b * a.pg.hkv + u.uk / a.HB : u.b;
+    const int64_t row = a.pg.per_head ? (int64_t)u.b * a.pg.hkv + u.kvh : u.b;
     return __ldg(a.table + row * a.max_pages + blk);
   }
   __device__ __forceinline__ int64_t checked(int page) const {
@@ -225,14 +234,18 @@ struct Worker {
   __device__ __forceinline__ void advance(Cursor& u) const {
     if (++u.tile == u.e.nt) {
       u.tile = 0;
-      if (++u.uk == a.pg.hkv * a.HB) {
-        u.uk = 0;
-        do {
-          u.e = extent<kTile>(a, ++u.b);
-        } while (u.e.nt == 0);
-      }
+      next_unit(u);
     }
     place(u);
+  }
+  __device__ __forceinline__ void next_unit(Cursor& u) const {
+    if (++u.hb < a.HB) return;
+    u.hb = 0;
+    if (++u.kvh < a.pg.hkv) return;
+    u.kvh = 0;
+    do {
+      u.e = extent<kTile>(a, ++u.b);
+    } while (u.e.nt == 0);
   }
 
   // Start the copies of the cursor's tile into ring stage `st`. Tokens outside [lo, len) are
@@ -241,10 +254,11 @@ struct Worker {
   __device__ __forceinline__ void issue(const Cursor& u, int st) const {
     const uint32_t base = ring + st * C::kStageBytes;
     const int t = (u.e.lo / kTile + u.tile) * kTile;
-    const int kvh = u.uk / a.HB;
+    const int kvh = u.kvh;
     constexpr int CPR = MX ? HD / 32 : HD / 8;  // 16-byte chunks per record
     constexpr int RP = 32 / CPR;                // records per instruction
     const int row0 = lane / CPR, ch = lane % CPR;
+    const bool full = t >= u.e.lo && t + kTile <= u.e.len;
 #pragma unroll
     for (int h = 0; h < kBlocksT; ++h) {
       int64_t off0 = 0, soff0 = 0;
@@ -265,7 +279,7 @@ struct Worker {
 #pragma unroll
       for (int j = 0; j < kRows / RP; ++j) {
         const int row = h * kRows + row0 + j * RP;
-        const bool ok = t + row >= u.e.lo && t + row < u.e.len;
+        const bool ok = full || (t + row >= u.e.lo && t + row < u.e.len);
         const int64_t off = WHOLE ? mine + j * RP * a.pg.tok_b : __shfl_sync(kFull, off0, row0 + j * RP) + ch * 16;
         const uint32_t dst = base + row * C::kPitch + (MX ? ch : (ch ^ chunk_swizzle(row))) * 16;
         cp_async<16>(dst, a.pg.k + off, ok);
@@ -273,7 +287,7 @@ struct Worker {
       }
       if constexpr (MX) {  // scales: lanes 0-15 key rows, 16-31 value rows of the block
         const int row = h * kRows + (lane & 15);
-        const bool ok = t + row >= u.e.lo && t + row < u.e.len;
+        const bool ok = full || (t + row >= u.e.lo && t + row < u.e.len);
         const int64_t off = WHOLE ? soff0 + times(lane & 15, a.pg.stok_b) : soff0;
         const uint8_t* src = (lane < 16 ? a.pg.ks : a.pg.vs) + off;
         const uint32_t dst = base + 2 * kTile * C::kPitch + ((lane < 16 ? 0 : kTile) + row) * C::kScale;
@@ -290,7 +304,7 @@ struct Worker {
   // ---- one unit's queries -------------------------------------------------------------
 
   __device__ __forceinline__ void begin(const Cursor& u) {
-    const int kvh = u.uk / a.HB, hb = u.uk - kvh * a.HB;
+    const int kvh = u.kvh, hb = u.hb;
     const int heads = min(a.GB, a.G - hb * a.GB);
     const int col = lane >> 2, head = SMALL ? col & 3 : col;
     const bool ok = head < heads;
@@ -363,8 +377,8 @@ struct Worker {
         uint32_t x[4], y[4];
         e2m1x8_f16(lds32(row + i * 16), x);
         e2m1x8_f16(lds32(row + 8 * C::kPitch + i * 16), y);
-        float g[4] = {0.f, 0.f, 0.f, 0.f};
-        mma16816<__half>(g, x[0], y[0], x[1], y[1], q[i][0], q[i][1]);
+        float g[4];
+        mma16816_new(g, x[0], y[0], x[1], y[1], q[i][0], q[i][1]);
         mma16816<__half>(g, x[2], y[2], x[3], y[3], q[i][2], q[i][3]);
         float f[2];
 #pragma unroll
@@ -681,7 +695,7 @@ struct Worker {
   }
 
   __device__ __forceinline__ void write_out(const Cursor& u) const {
-    const int kvh = u.uk / a.HB, hb = u.uk - kvh * a.HB;
+    const int kvh = u.kvh, hb = u.hb;
     const int heads = min(a.GB, a.G - hb * a.GB);
     const int64_t row0 = (int64_t)u.b * a.hq + kvh * a.G + hb * a.GB;
     each(heads, [&](int h, int j, int d0, const float (&x)[8]) {
@@ -826,8 +840,9 @@ __global__ void __launch_bounds__(Config<FMT, HD>::kWarps * 32, 1) kv_decode_ker
       start += (int64_t)cur.e.nt * upb;
       cur.e = extent<C::kTile>(a, ++cur.b);
     }
-    cur.uk = (int)quotient(r0 - start, cur.e.nt);
-    cur.tile = (int)(r0 - start - (int64_t)cur.uk * cur.e.nt);
+    const int uk = (int)quotient(r0 - start, cur.e.nt);
+    cur.kvh = uk / a.HB, cur.hb = uk - cur.kvh * a.HB;
+    cur.tile = (int)(r0 - start - (int64_t)uk * cur.e.nt);
     ld = cur;
     wk.place(ld);
     int64_t left = r1 - r0;  // tiles not yet issued
@@ -861,22 +876,16 @@ __global__ void __launch_bounds__(Config<FMT, HD>::kWarps * 32, 1) kv_decode_ker
         if (seg_from == 0) {
           wk.write_out(cur);
         } else if (i + 1 < r1) {       // begun by another warp: leave the piece for the merge
-          const int hb = cur.uk % a.HB;
-          wk.write_piece(a.head + gw * a.GB * kRow, min(a.GB, a.G - hb * a.GB));
+          wk.write_piece(a.head + gw * a.GB * kRow, min(a.GB, a.G - cur.hb * a.GB));
           if (lane == 0) {
-            s_pb[2 * w] = cur.b, s_uk[2 * w] = cur.uk, s_from[2 * w] = seg_from, s_to[2 * w] = cur.e.nt;
+            s_pb[2 * w] = cur.b, s_uk[2 * w] = cur.kvh * a.HB + cur.hb, s_from[2 * w] = seg_from, s_to[2 * w] = cur.e.nt;
             s_nt[2 * w] = cur.e.nt, s_tile0[2 * w] = r0;
           }
         }
         open = seg_from != 0 && i + 1 == r1;
         if (i + 1 < r1) {
           cur.tile = 0;
-          if (++cur.uk == upb) {
-            cur.uk = 0;
-            do {
-              cur.e = extent<C::kTile>(a, ++cur.b);
-            } while (cur.e.nt == 0);
-          }
+          wk.next_unit(cur);
           seg_from = 0;
           wk.begin(cur);
           open = true;
@@ -892,11 +901,10 @@ __global__ void __launch_bounds__(Config<FMT, HD>::kWarps * 32, 1) kv_decode_ker
   __syncthreads();  // every ring is idle: its memory holds the last pieces from here on
   float* pieces = reinterpret_cast<float*>(smem);
   if (open) {
-    const int hb = cur.uk % a.HB;
-    wk.write_piece(pieces + w * a.GB * kRow, min(a.GB, a.G - hb * a.GB));
+    wk.write_piece(pieces + w * a.GB * kRow, min(a.GB, a.G - cur.hb * a.GB));
     if (lane == 0) {
       const int i = 2 * w + 1;
-      s_pb[i] = cur.b, s_uk[i] = cur.uk, s_from[i] = seg_from, s_to[i] = cur.tile + 1, s_nt[i] = cur.e.nt;
+      s_pb[i] = cur.b, s_uk[i] = cur.kvh * a.HB + cur.hb, s_from[i] = seg_from, s_to[i] = cur.tile + 1, s_nt[i] = cur.e.nt;
       s_tile0[i] = r1 - (cur.tile + 1 - seg_from);
     }
   }
