@@ -173,8 +173,8 @@ __device__ __forceinline__ Extent extent(const DecArgs& a, int b) {
 struct Cursor {
   Extent e;
   int b, kvh, hb, tile;
-  int off[2];   // pages of whole row blocks: place of each block's first token in its page,
-  int page[2];  // and the page's entry of the block table, loaded ahead of its use and checked then
+  int off[2];   // place in its page of each row block's first token (pages of whole blocks), or of
+  int page[2];  // the lane's token in it; the page's table entry, loaded a tile ahead, checked at use
 };
 
 template <typename T, int FMT, int HD, bool SMALL, bool WHOLE>
@@ -220,15 +220,18 @@ struct Worker {
   // Look up the pages of the cursor's tile (a row block past the sequence's end stands in the
   // last one's place: none of its tokens is read).
   __device__ __forceinline__ void place(Cursor& u) const {
-    if constexpr (WHOLE) {
 #pragma unroll
-      for (int h = 0; h < kBlocksT; ++h) {
-        int t = (u.e.lo / kTile + u.tile) * kTile + h * kRows;
+    for (int h = 0; h < kBlocksT; ++h) {
+      int t = (u.e.lo / kTile + u.tile) * kTile + h * kRows;
+      if constexpr (WHOLE) {
         if (h && t >= u.e.len) t -= kRows;
-        const int blk = a.pg.page_shift >= 0 ? t >> a.pg.page_shift : t / (int)a.pg.page_size;
-        u.off[h] = t - blk * (int)a.pg.page_size;
-        u.page[h] = page_of(u, blk);
+      } else {  // 16 lanes look up a block's tokens, and share what they find in issue
+        t += lane & 15;
+        t = t < u.e.lo ? u.e.lo : t >= u.e.len ? u.e.len - 1 : t;
       }
+      const int blk = a.pg.page_shift >= 0 ? t >> a.pg.page_shift : t / (int)a.pg.page_size;
+      u.off[h] = t - blk * (int)a.pg.page_size;
+      u.page[h] = page_of(u, blk);
     }
   }
   __device__ __forceinline__ void advance(Cursor& u) const {
@@ -261,20 +264,10 @@ struct Worker {
     const bool full = t >= u.e.lo && t + kTile <= u.e.len;
 #pragma unroll
     for (int h = 0; h < kBlocksT; ++h) {
-      int64_t off0 = 0, soff0 = 0;
-      if constexpr (WHOLE) {
-        const uint32_t pg = (uint32_t)checked(u.page[h]);
-        off0 = times(pg, a.pg.page_b) + times(u.off[h], a.pg.tok_b) + times(kvh, a.pg.head_b);
-        if constexpr (MX) soff0 = times(pg, a.pg.spage_b) + times(u.off[h], a.pg.stok_b) + times(kvh, a.pg.shead_b);
-      } else {
-        // each of 16 lanes looks up one token's page; the others receive it by shuffles
-        int tok = t + h * kRows + (lane & 15);
-        tok = tok < u.e.lo ? u.e.lo : tok >= u.e.len ? u.e.len - 1 : tok;
-        const int blk = tok / (int)a.pg.page_size, o = tok - blk * (int)a.pg.page_size;
-        const uint32_t pg = (uint32_t)checked(page_of(u, blk));
-        off0 = times(pg, a.pg.page_b) + times(o, a.pg.tok_b) + times(kvh, a.pg.head_b);
-        if constexpr (MX) soff0 = times(pg, a.pg.spage_b) + times(o, a.pg.stok_b) + times(kvh, a.pg.shead_b);
-      }
+      const uint32_t pg = (uint32_t)checked(u.page[h]);
+      const int64_t off0 = times(pg, a.pg.page_b) + times(u.off[h], a.pg.tok_b) + times(kvh, a.pg.head_b);
+      int64_t soff0 = 0;
+      if constexpr (MX) soff0 = times(pg, a.pg.spage_b) + times(u.off[h], a.pg.stok_b) + times(kvh, a.pg.shead_b);
       const int64_t mine = off0 + (WHOLE ? times(row0, a.pg.tok_b) : 0) + ch * 16;
 #pragma unroll
       for (int j = 0; j < kRows / RP; ++j) {
