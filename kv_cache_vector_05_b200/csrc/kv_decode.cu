@@ -729,11 +729,12 @@ __device__ __forceinline__ void store4(const DecArgs& a, bool f16, int64_t at, f
   }
 }
 
-// total * i / n, in 32 bits where they suffice.
-__device__ __forceinline__ int64_t scaled(int64_t total, int64_t i, int64_t n) {
-  const int64_t x = total * i;
-  return (total * n >> 32) == 0 ? (int64_t)((uint32_t)x / (uint32_t)n) : x / n;
+// x / n for x >= 0, n > 0, in 32 bits where they suffice (a 64-bit division is several hundred
+// cycles on the way to the first load).
+__device__ __forceinline__ int64_t divided(int64_t x, int64_t n) {
+  return ((x | n) >> 32) == 0 ? (int64_t)((uint32_t)x / (uint32_t)n) : x / n;
 }
+__device__ __forceinline__ int64_t scaled(int64_t total, int64_t i, int64_t n) { return divided(total * i, n); }
 
 __device__ __forceinline__ int64_t warp_incl_scan(int64_t v, int lane) {
 #pragma unroll
@@ -764,7 +765,7 @@ __global__ void __launch_bounds__(Config<FMT, HD>::kWarps * 32, 1) kv_decode_ker
   int n;
   auto divide = [&](int64_t all) {
     total = all * upb;
-    const int64_t want = (total + W * C::kMinTiles - 1) / (W * C::kMinTiles);
+    const int64_t want = divided(total + W * C::kMinTiles - 1, W * C::kMinTiles);
     n = (int)(want < gridDim.x ? want : gridDim.x);
     cta0 = n ? scaled(total, k, n) : 0;
   };
@@ -834,7 +835,7 @@ __global__ void __launch_bounds__(Config<FMT, HD>::kWarps * 32, 1) kv_decode_ker
       cur.e = extent<C::kTile>(a, ++cur.b);
     }
     const int uk = (int)quotient(r0 - start, cur.e.nt);
-    cur.kvh = uk / a.HB, cur.hb = uk - cur.kvh * a.HB;
+    cur.kvh = a.HB == 1 ? uk : uk / a.HB, cur.hb = uk - cur.kvh * a.HB;
     cur.tile = (int)(r0 - start - (int64_t)uk * cur.e.nt);
     ld = cur;
     wk.place(ld);
@@ -910,7 +911,7 @@ __global__ void __launch_bounds__(Config<FMT, HD>::kWarps * 32, 1) kv_decode_ker
     const int i = __ffs(todo) - 1, b = __shfl_sync(kFull, pb, i), uk = __shfl_sync(kFull, puk, i);
     const uint32_t run = todo & __ballot_sync(kFull, pb == b && puk == uk);
     todo &= ~run;
-    const int last = 31 - __clz(run), kvh = uk / a.HB, hb = uk - kvh * a.HB;
+    const int last = 31 - __clz(run), kvh = a.HB == 1 ? uk : uk / a.HB, hb = uk - kvh * a.HB;
     const int heads = min(a.GB, a.G - hb * a.GB);
     const bool whole = s_from[i] == 0 && s_to[last] == s_nt[i];
     const int64_t row0 = (int64_t)b * a.hq + kvh * a.G + hb * a.GB;
@@ -948,7 +949,7 @@ __global__ void __launch_bounds__(Config<FMT, HD>::kWarps * 32, 1) kv_decode_ker
     }
     if (!whole && s_from[i] == 0 && tid == 0) {  // begun here, ended by a later CTA
       const int64_t end = s_tile0[i] + s_nt[i];
-      a.meta[k] = make_int4(b, uk, (int)((end * n - 1) / total), 1 + (s_tile0[i] == cta0 ? 0 : 1));
+      a.meta[k] = make_int4(b, uk, (int)divided(end * n - 1, total), 1 + (s_tile0[i] == cta0 ? 0 : 1));
     }
   }
 
@@ -973,7 +974,7 @@ __global__ void __launch_bounds__(256) kv_combine_kernel(const DecArgs a, int f1
   const int k0 = blockIdx.x, h = blockIdx.y;
   const int4 mt = a.meta[k0];
   if (!mt.w) return;
-  const int kvh = mt.y / a.HB, hb = mt.y - kvh * a.HB;
+  const int kvh = a.HB == 1 ? mt.y : mt.y / a.HB, hb = mt.y - kvh * a.HB;
   if (h >= a.G - hb * a.GB) return;
   const int g = threadIdx.x / kLanes, x = threadIdx.x % kLanes, count = mt.z - k0 + 1;
   auto row = [&](int i) {
