@@ -225,6 +225,10 @@ __global__ void __launch_bounds__(Config<MODE, HD>::kThreads, 1) kv_prefill_kern
   extern __shared__ unsigned char smem_raw[];
   unsigned char* sm = reinterpret_cast<unsigned char*>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
   const int tid = threadIdx.x, warp = __shfl_sync(kFull, tid >> 5, 0), lane = tid & 31;
+  if (MODE == kTma && tid == 288) {
+    asm volatile("prefetch.tensormap [%0];" ::"l"(&a.kmap) : "memory");
+    asm volatile("prefetch.tensormap [%0];" ::"l"(&a.vmap) : "memory");
+  }
   const Block w = locate<ROWS>(a, tid == 0);
   if (!w.ok || w.first >= w.rows) return;
 
@@ -286,15 +290,23 @@ __global__ void __launch_bounds__(Config<MODE, HD>::kThreads, 1) kv_prefill_kern
   uint64_t* b_free = bars + 9 + NS;
   uint64_t* b_raw = bars + 9 + 2 * NS;  // [NS] kTma: a V tile with an edge has landed
   volatile uint32_t* ctl = reinterpret_cast<volatile uint32_t*>(bars + 9 + 3 * NS);  // tmem, dirty
-  if (MODE == kTma && tid == 288) {
-    asm volatile("prefetch.tensormap [%0];" ::"l"(&a.kmap) : "memory");
-    asm volatile("prefetch.tensormap [%0];" ::"l"(&a.vmap) : "memory");
-  }
+  // kTma: lane c looks up the page of box c (of both K and V); the first tile's before the set-up
+  const int32_t* trow = a.table + (a.pg.per_head ? (int64_t)w.b * a.pg.hkv + w.kvh : (int64_t)w.b) * a.max_pages;
+  int box_page = 0, box_off = 0;
+  bool box_live = false;
+  auto look_box = [&](int tile) {
+    const int tok = tile * BN + lane * a.box;
+    box_live = lane < BN / a.box && tok < hi && tok + a.box > lo;
+    const int blk = !box_live ? 0 : a.pg.page_shift >= 0 ? tok >> a.pg.page_shift : tok / (int)a.pg.page_size;
+    box_off = tok - blk * (int)a.pg.page_size;
+    if (box_live) box_page = __ldg(trow + blk);
+  };
+  if (MODE == kTma && warp >= 9 && n_tiles > 0) look_box(t0);
   if (warp == 8) {
     tmem_alloc(const_cast<uint32_t*>(ctl), 512);
     tmem_relinquish();
   }
-  if (tid == 0) {
+  if (tid == 320) {
     ctl[1] = 0;
     mbar_init(b_q, 256);
     for (int t = 0; t < 2; ++t) {
@@ -322,26 +334,15 @@ __global__ void __launch_bounds__(Config<MODE, HD>::kThreads, 1) kv_prefill_kern
   };
 
   if (warp >= 8) {
-    if constexpr (!MX) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kLess));
+    if (!MX) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kLess));
     if (warp >= 9 && n_tiles > 0) {
       // ---- loaders --------------------------------------------------------------------
       const int lt = tid - 288;
-      const int32_t* trow = a.table + (a.pg.per_head ? (int64_t)w.b * a.pg.hkv + w.kvh : (int64_t)w.b) * a.max_pages;
       if constexpr (MODE == kTma) {
-        // Lane c looks up the page of box c (of both K and V) a tile ahead; box (c, 64-column panel
-        // p) of a tile is issued by warp 9 + (c * panels + p) % 3 (one issue takes a warp about
+        // Pages are looked up a tile ahead; box (c, 64-column panel p) of a tile is issued by warp 9 + (c * panels + p) % 3 (one issue takes a warp about
         // 100 cycles, since its operands differ from box to box). Warp 9 announces the bytes.
         constexpr int NP = HD / 64;
         const int per_tile = BN / a.box, me = warp - 9;
-        int pid = 0, off = 0;
-        bool live = false;
-        auto look = [&](int tile) {
-          const int tok = tile * BN + lane * a.box;
-          live = lane < per_tile && tok < hi && tok + a.box > lo;
-          const int blk = live ? tok / (int)a.pg.page_size : 0;
-          off = tok - blk * (int)a.pg.page_size;
-          if (live) pid = __ldg(trow + blk);
-        };
         uint32_t seen = 0;  // parity of each stage's b_raw
         // edge tiles of V: zero what is not finite, and the rows of tokens that no row here sees
         auto mend = [&](int j) {
@@ -363,15 +364,14 @@ __global__ void __launch_bounds__(Config<MODE, HD>::kThreads, 1) kv_prefill_kern
           named_sync<kLoaders>();
           if (lt == 0) mbar_arrive(b_full + st);
         };
-        look(t0);
         for (int j = 0; j < n_tiles; ++j) {
-          if (live && (pid < 0 || pid >= a.pg.n_pages)) {
+          if (box_live && (box_page < 0 || box_page >= a.pg.n_pages)) {
             if (me == 0) atomicOr(a.err, kErrIndex);
-            pid = 0;
+            box_page = 0;
           }
-          const uint32_t boxes = __ballot_sync(kFull, live);
-          const int pg = pid, of = off;
-          if (j + 1 < n_tiles) look(t0 + j + 1);
+          const uint32_t boxes = __ballot_sync(kFull, box_live);
+          const int pg = box_page, of = box_off;
+          if (j + 1 < n_tiles) look_box(t0 + j + 1);
 #pragma unroll
           for (int kv = 0; kv < 2; ++kv) {
             const int h = 2 * j + kv, st = h % NS;
@@ -595,7 +595,7 @@ __global__ void __launch_bounds__(Config<MODE, HD>::kThreads, 1) kv_prefill_kern
       }
     }
   } else {
-    if constexpr (!MX) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kMore));
+    if (!MX) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kMore));
     if (n_tiles > 0) {
       cp_wait<0>();
       fence_async_smem();
