@@ -52,12 +52,12 @@ __device__ __forceinline__ void unpack8(const uint4& x, float2 (&y)[4]) {
   y[2] = Half2<T>::unpack(x.z), y[3] = Half2<T>::unpack(x.w);
 }
 
-// Rotate a chunk in place. Halves: its own coordinates times cosines plus the pairs' others times
+// Rotate a chunk in place (with scalar products and sums: paired ones were seen to be fused).
+// Halves: its own coordinates times cosines plus the pairs' others times
 // signed sines (-sin where the chunk holds the first coordinates: a c + b (-s) rounds like
 // a c - b s). Interleaved: the pairs lie in the chunk, c and s hold their four angles.
 template <typename T, bool INTER, int N>
 __device__ __forceinline__ void turn(float2 (&y)[4], const uint4& par, const float2 (&c)[N], const float2 (&s)[N]) {
-  using namespace sm100;
   if constexpr (INTER) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -70,7 +70,10 @@ __device__ __forceinline__ void turn(float2 (&y)[4], const uint4& par, const flo
     float2 z[4];
     unpack8<T>(par, z);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) y[i] = add2(mul2(y[i], c[i]), mul2(z[i], s[i]));
+    for (int i = 0; i < 4; ++i) {
+      y[i].x = __fadd_rn(__fmul_rn(y[i].x, c[i].x), __fmul_rn(z[i].x, s[i].x));
+      y[i].y = __fadd_rn(__fmul_rn(y[i].y, c[i].y), __fmul_rn(z[i].y, s[i].y));
+    }
   }
 }
 

@@ -98,7 +98,7 @@ __device__ __forceinline__ float ex2(float x) {
 template <typename T>
 __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                          uint32_t b0, uint32_t b1) {
-  if constexpr (sizeof(T) == 2 && std::is_same<T, __half>::value)
+  if constexpr (std::is_same<T, __half>::value)
     asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
@@ -108,12 +108,18 @@ __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// d = A B for f16 operands (no accumulator to clear).
+// d = A B (no accumulator to clear).
+template <typename T>
 __device__ __forceinline__ void mma16816_new(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                              uint32_t b0, uint32_t b1) {
-  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
-      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+  if constexpr (std::is_same<T, __half>::value)
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+  else
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
 }
 
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
@@ -371,7 +377,7 @@ struct Worker {
         e2m1x8_f16(lds32(row + i * 16), x);
         e2m1x8_f16(lds32(row + 8 * C::kPitch + i * 16), y);
         float g[4];
-        mma16816_new(g, x[0], y[0], x[1], y[1], q[i][0], q[i][1]);
+        mma16816_new<__half>(g, x[0], y[0], x[1], y[1], q[i][0], q[i][1]);
         mma16816<__half>(g, x[2], y[2], x[3], y[3], q[i][2], q[i][3]);
         float f[2];
 #pragma unroll
@@ -422,9 +428,12 @@ struct Worker {
     }
   }
 
-  // acc += V^T P for the terms b[0], b[1] (SMALL: together in b[0]) and, if `third`, b[2].
-  template <bool SLOW>
-  __device__ __forceinline__ void values(uint32_t base, int h, const uint32_t (&b)[3][2], bool third) {
+  // acc += V^T P for the terms b[0], b[1] (SMALL: together in b[0]) and, bf16, b[2]. FINE: for fp32
+  // output; a row block's products are summed apart and added to acc by rounded fp32 additions (the
+  // tensor cores truncate theirs, which over 1M tokens adds up to 4e-6 of the output), and bf16
+  // terms are three.
+  template <bool SLOW, bool FINE>
+  __device__ __forceinline__ void values(uint32_t base, int h, const uint32_t (&b)[3][2]) {
     const uint32_t v = base + (kTile + h * kRows) * C::kPitch;
     constexpr int NC = HD / 64;  // 8-coordinate chunks per lane and token
     using TV = typename std::conditional<MX, typename std::conditional<SLOW, __nv_bfloat16, __half>::type, T>::type;
@@ -470,11 +479,17 @@ struct Worker {
         interleave4<SLOW>(x[2], x[3], f[1], hi);
       }
     };
-    auto product = [&](float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
-      mma16816<TV>(d, a0, a1, a2, a3, b[0][0], b[0][1]);
+    constexpr bool kThird = FINE && std::is_same<TV, __nv_bfloat16>::value;
+    auto product = [&](float (&sum)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
+      float part[4];
+      float(&d)[4] = FINE ? part : sum;
+      if constexpr (FINE) mma16816_new<TV>(d, a0, a1, a2, a3, b[0][0], b[0][1]);
+      else mma16816<TV>(d, a0, a1, a2, a3, b[0][0], b[0][1]);
       if constexpr (!SMALL) mma16816<TV>(d, a0, a1, a2, a3, b[1][0], b[1][1]);
-      if (SLOW || FMT == TQ_KV_BF16)
-        if (third) mma16816<TV>(d, a0, a1, a2, a3, b[2][0], b[2][1]);
+      if constexpr (kThird) mma16816<TV>(d, a0, a1, a2, a3, b[2][0], b[2][1]);
+      if constexpr (FINE)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) sum[i] += part[i];
     };
     if constexpr (NC == 1) {
       uint32_t lo[8], hi[8];
@@ -573,16 +588,17 @@ struct Worker {
 #pragma unroll
         for (int i = 0; i < 4; ++i) p[i] *= f;
         split<__nv_bfloat16, 3>(p, b);
-        values<true>(base, h, b, true);
+        values<true, true>(base, h, b);
       } else if constexpr (F16P) {
         split<__half, 2>(p, b);
-        values<false>(base, h, b, false);
+        if (a.out_f32) values<false, true>(base, h, b);
+        else values<false, false>(base, h, b);
       } else if (a.out_f32) {
         split<__nv_bfloat16, 3>(p, b);
-        values<false>(base, h, b, true);
+        values<false, true>(base, h, b);
       } else {
         split<__nv_bfloat16, 2>(p, b);
-        values<false>(base, h, b, false);
+        values<false, false>(base, h, b);
       }
     }
   }
