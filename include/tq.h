@@ -262,7 +262,7 @@ tq_status tq_merge_attention(const float* outs, int64_t outs_stride, const float
  * complete in time sets this word, abandons the rest of its work and exits, so
  * the CUDA context stays usable. Returns TQ_ECUDA (with tq_last_error() saying
  * which wait) if any call since the last check hit such a timeout, TQ_EINVAL if a
- * slot or page index was out of range, TQ_OK otherwise. */
+ * slot, page, position or row range was out of bounds, TQ_OK otherwise. */
 tq_status tq_check_device(const tq_ctx* ctx, void* stream);
 
 /* Decode attention that allocates nothing and takes no workspace. The pages describe

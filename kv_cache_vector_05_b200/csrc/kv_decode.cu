@@ -70,6 +70,10 @@ struct DecArgs {
   unsigned int* err;
 };
 
+// MXFP4: ref is set this far above the largest scale seen, and never below kRefLeast, so that p
+// 2^(140 - ref) of a SLOW tile stays below 2^127.
+constexpr int kRefSlack = 3, kRefLeast = 32;
+
 // Format, head dimension -> warps per CTA and ring stages (one CTA per SM).
 template <int FMT, int HD>
 struct Config {
@@ -195,9 +199,6 @@ struct Worker {
   static constexpr bool F16P = FMT != TQ_KV_BF16;
   static constexpr float kOff = F16P ? 13.f : 0.f;
   static constexpr float kSlack = F16P ? 2.f : 8.f;
-  // ref is set this far above the largest scale seen, and never below kRefLeast, so that p 2^(140 -
-  // ref) of a SLOW tile stays below 2^127
-  static constexpr int kRefSlack = 3, kRefLeast = 32;
 
   const DecArgs& a;
   const int lane, r, c;
@@ -223,13 +224,14 @@ struct Worker {
     return 0;
   }
 
-  // Look up the pages of the cursor's tile (a row block past the sequence's end stands in the
-  // last one's place: none of its tokens is read).
+  // Look up the pages of the cursor's tile. A row block before the window or past the sequence's
+  // end stands in its neighbour's place: none of its tokens is read, nor its table entry.
   __device__ __forceinline__ void place(Cursor& u) const {
 #pragma unroll
     for (int h = 0; h < kBlocksT; ++h) {
       int t = (u.e.lo / kTile + u.tile) * kTile + h * kRows;
       if constexpr (WHOLE) {
+        if (t + kRows <= u.e.lo) t += kRows;
         if (h && t >= u.e.len) t -= kRows;
       } else {  // 16 lanes look up a block's tokens, and share what they find in issue
         t += lane & 15;

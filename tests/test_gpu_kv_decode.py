@@ -279,6 +279,26 @@ def test_decode_bad_page_is_reported_and_lengths_are_clamped():
         assert torch.equal(out, want)
 
 
+@pytest.mark.parametrize("fmt,page,window", [("mxfp4", 16, 20), ("mxfp4", 16, 1), ("mxfp4", 48, 70), ("mxfp4", 5, 33),
+                                             ("bf16", 16, 17), ("f16", 24, 30)])
+def test_decode_window_reads_no_entry_before_it(fmt, page, window):
+    """Pages that lie wholly before the window may be gone: their table entries are never read."""
+    d, hkv, g = 64, 1, 2
+    rng = np.random.default_rng(10)
+    ctx = make_ctx(d)
+    lens = np.arange(1, 140)
+    cache = random_cache(rng, fmt, int((-(-lens // page)).sum()), page, hkv, d, False)
+    table = block_tables(rng, lens, page, hkv, False, -(-140 // page), cache[0].shape[0])
+    gone = table.copy()
+    for b, n in enumerate(lens):
+        gone[b, :max(0, n - window) // page] = -1
+    q = torch.randn((len(lens), hkv * g, d), device=DEV).to(P.TORCH[fmt])
+    out, lse = T.tq_decode_kv_pages(ctx, q, T.KVPages(*cache), hkv, up(gone), 139, seq_lens=up(lens.astype(np.int32)),
+                                    window=window)
+    T.tq_check_device(ctx)
+    check(cache, table, lens, q, out, lse, page, False, hkv, window, fmt, "f32")
+
+
 def test_decode_without_lengths_and_max_len_zero():
     d, hkv, g, page = 128, 1, 2, 16
     rng = np.random.default_rng(7)

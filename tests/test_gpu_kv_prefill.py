@@ -192,6 +192,24 @@ def test_prefill_large_and_rising_logits(fmt):
     check(cache, table, q_lens, kv_lens, cu, q, out, lse, 16, False, hkv, 0, fmt)
 
 
+@pytest.mark.parametrize("fmt,page,window", [("bf16", 16, 40), ("bf16", 20, 40), ("mxfp4", 16, 40), ("f16", 128, 1)])
+def test_prefill_window_reads_no_entry_before_it(fmt, page, window):
+    """Pages that lie wholly before the first new row's window may be gone, as may those of
+    positions past the sequence."""
+    d, g, hkv = 64, 2, 1
+    rng = np.random.default_rng(18)
+    ctx = make_ctx(d)
+    q_lens, kv_lens, cache, table, cu, q = simple(rng, fmt, d, g, hkv, [(7, 400), (130, 900), (1, 129), (300, 300)],
+                                                  page=page, max_len=1000)
+    gone = table.copy()
+    for b, (nq, n) in enumerate(zip(q_lens, kv_lens)):
+        gone[b, :max(0, n - nq - window + 1) // page] = -1
+    out, lse = T.tq_prefill_kv_pages(ctx, q, T.KVPages(*cache), hkv, up(gone), 1000, up(cu), 300,
+                                     seq_lens=up(kv_lens.astype(np.int32)), window=window)
+    T.tq_check_device(ctx)
+    check(cache, table, q_lens, kv_lens, cu, q, out, lse, page, False, hkv, window, fmt)
+
+
 def test_prefill_one_row_equals_decode():
     """A chunk of one token per sequence is a decode step (up to P's rounding)."""
     d, g, hkv = 128, 4, 2
