@@ -464,10 +464,13 @@ tq_status tq_decode_kv_pages(const tq_ctx* ctx, const tq_kv_pages* pages, const 
                              void* out, tq_dtype out_dtype, float* lse, void* workspace, size_t workspace_bytes,
                              void* stream);
 
-/* Bytes of device workspace tq_prefill_kv_pages needs (may be 0: then workspace may be
- * NULL). Also 0 for invalid arguments. */
-size_t tq_prefill_kv_pages_workspace_bytes(const tq_ctx* ctx, int64_t total_q, int batch, int hq, int hkv,
-                                           int64_t max_len, int64_t max_q);
+/* Bytes of device workspace tq_prefill_kv_pages needs over a cache of `format` (may be 0:
+ * then workspace may be NULL). Also 0 for invalid arguments. It holds the partial results of
+ * short chunks, whose tokens are split over the SMs, and for long chunks over MXFP4 pages the
+ * attended tokens as bf16 vectors, batch * hkv * max_len * 4 d bytes, where that is at most
+ * 1 GiB. */
+size_t tq_prefill_kv_pages_workspace_bytes(const tq_ctx* ctx, tq_kv_format format, int64_t total_q, int batch,
+                                           int hq, int hkv, int64_t max_len, int64_t max_q);
 
 /* Causal attention of a chunk of new tokens per sequence over a page cache that already
  * holds them (tq_append_kv_pages): the whole prompt, a later chunk of it, or several

@@ -143,7 +143,7 @@ def _load() -> ctypes.CDLL:
     lib.tq_decode_kv_pages.argtypes = [vp, pages, vp, c_int, i64, c_int, c_int, vp, i64, vp, i64, i64,
                                        ctypes.c_float, vp, c_int, vp, vp, sz, vp]
     lib.tq_decode_kv_pages.restype = c_int
-    lib.tq_prefill_kv_pages_workspace_bytes.argtypes = [vp, i64, c_int, c_int, c_int, i64, i64]
+    lib.tq_prefill_kv_pages_workspace_bytes.argtypes = [vp, c_int, i64, c_int, c_int, c_int, i64, i64]
     lib.tq_prefill_kv_pages_workspace_bytes.restype = sz
     lib.tq_prefill_kv_pages.argtypes = [vp, pages, vp, c_int, i64, i64, c_int, c_int, vp, i64, vp, i64, vp, i64, i64,
                                         ctypes.c_float, vp, vp, vp, sz, vp]
@@ -703,8 +703,9 @@ def tq_decode_kv_pages(ctx: Context, q, pages: KVPages, hkv: int, block_table, m
 
 
 def tq_prefill_kv_pages_workspace_bytes(ctx: Context, total_q: int, batch: int, hq: int, hkv: int, max_len: int,
-                                        max_q: int) -> int:
-    return int(lib.tq_prefill_kv_pages_workspace_bytes(ctx.handle, total_q, batch, hq, hkv, max_len, max_q))
+                                        max_q: int, kv_format: int = TQ_KV_MXFP4) -> int:
+    """Workspace of tq_prefill_kv_pages over a cache of `kv_format` (the default's is enough for any)."""
+    return int(lib.tq_prefill_kv_pages_workspace_bytes(ctx.handle, kv_format, total_q, batch, hq, hkv, max_len, max_q))
 
 
 def tq_prefill_kv_pages(ctx: Context, q, pages: KVPages, hkv: int, block_table, max_len: int, cu_q, max_q: int,
@@ -728,7 +729,7 @@ def tq_prefill_kv_pages(ctx: Context, q, pages: KVPages, hkv: int, block_table, 
         lse = torch.empty((total_q, hq), dtype=torch.float32, device=q.device)
     need = 0
     if workspace is None:
-        need = lib.tq_prefill_kv_pages_workspace_bytes(ctx.handle, total_q, batch, hq, hkv, max_len, max_q)
+        need = tq_prefill_kv_pages_workspace_bytes(ctx, total_q, batch, hq, hkv, max_len, max_q, pages.format)
     workspace = _workspace(workspace, need, pages)
     status = lib.tq_prefill_kv_pages(
         ctx.handle, p, q.data_ptr(), pages.code, qs, total_q, batch, hq, starts, max_q, table, block_table.shape[-1],

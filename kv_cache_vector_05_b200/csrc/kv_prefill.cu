@@ -848,6 +848,66 @@ __global__ void __launch_bounds__(256) kv_prefill_combine_kernel(const __grid_co
   if (a.lse && lane == 0) a.lse[row] = (m + log2f(l)) * kLn2;
 }
 
+struct ExpandArgs {
+  PreArgs a;
+  char* k;        // [batch][hkv][room][d] bf16
+  char* v;
+  int32_t* table; // [batch * hkv]: each (sequence, KV head) is a page of its own
+  int64_t room;   // tokens per (sequence, KV head)
+};
+
+constexpr int kExpandTokens = 32;  // per block: 8 warps, a key and a value record of LPV lanes at a time
+
+// MXFP4 pages as bf16 vectors in token order, for the tokens some new row attends to: chunks of many
+// row blocks read each token's record once here, and the vectors by TMA as often as they have blocks.
+template <int HD>
+__global__ void __launch_bounds__(256) kv_expand_kernel(const __grid_constant__ ExpandArgs x) {
+  constexpr int LPV = HD / 8, VP = 32 / LPV, IT = kExpandTokens / (8 * VP);
+  const PreArgs& a = x.a;
+  const int unit = blockIdx.y, b = unit / a.pg.hkv, kvh = unit - b * a.pg.hkv;
+  if (blockIdx.x == 0 && threadIdx.x == 0) x.table[unit] = unit;
+  const int64_t s = __ldg(a.cu_q + b), e = __ldg(a.cu_q + b + 1);
+  if (s < 0 || e < s || e > a.total_q || e - s > a.max_q) return;  // reported by the main kernel
+  int64_t n = a.lens ? (int64_t)__ldg(a.lens + b) : a.max_len;
+  n = n < 0 ? 0 : n > a.max_len ? a.max_len : n;
+  const int64_t first = n - (e - s) - a.window + 1, lo = a.window && first > 0 ? first : 0;
+  const int lane = threadIdx.x & 31, ch = lane % LPV;
+  const int32_t* trow = a.table + (a.pg.per_head ? (int64_t)unit : (int64_t)b) * a.max_pages;
+  const int64_t t0 = (int64_t)blockIdx.x * kExpandTokens + (threadIdx.x >> 5) * (VP * IT) + lane / LPV;
+  uint32_t code[2 * IT], sc[2 * IT];
+#pragma unroll
+  for (int i = 0; i < IT; ++i) {
+    const int64_t t = t0 + i * VP;
+    if (t < lo || t >= n) continue;
+    const int64_t blk = a.pg.page_shift >= 0 ? t >> a.pg.page_shift : t / a.pg.page_size;
+    uint32_t p = (uint32_t)__ldg(trow + blk);
+    if (p >= (uint32_t)a.pg.n_pages) {
+      atomicOr(a.err, kErrIndex);
+      p = 0;
+    }
+    const uint32_t o = (uint32_t)(t - blk * a.pg.page_size);
+    const int64_t at = times(p, a.pg.page_b) + times(o, a.pg.tok_b) + times(kvh, a.pg.head_b) + ch * 4;
+    const int64_t sat = times(p, a.pg.spage_b) + times(o, a.pg.stok_b) + times(kvh, a.pg.shead_b) + ch / 4;
+    code[2 * i] = __ldg(reinterpret_cast<const uint32_t*>(a.pg.k + at)), sc[2 * i] = __ldg(a.pg.ks + sat);
+    code[2 * i + 1] = __ldg(reinterpret_cast<const uint32_t*>(a.pg.v + at)), sc[2 * i + 1] = __ldg(a.pg.vs + sat);
+  }
+#pragma unroll
+  for (int i = 0; i < 2 * IT; ++i) {
+    const int64_t t = t0 + (i >> 1) * VP;
+    if (t < lo || t >= n) continue;
+    uint32_t h[4], r[4];
+    e2m1x8_f16(code[i], h);
+    const float f = e8m0(sc[i]);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float2 y = mul2(Half2<__half>::unpack(h[j]), make_float2(f, f));
+      r[j] = Half2<__nv_bfloat16>::pack(y.x, y.y);
+    }
+    *reinterpret_cast<uint4*>((i & 1 ? x.v : x.k) + ((int64_t)unit * x.room + t) * (HD * 2) + ch * 16) =
+        make_uint4(r[0], r[1], r[2], r[3]);
+  }
+}
+
 // cuTensorMapEncodeTiled, fetched once from the driver through the runtime.
 using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
                                    const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
@@ -940,12 +1000,37 @@ int split_count(const tq_ctx* ctx, int batch, int G, int hkv, int64_t max_len, i
   return (int)std::max<int64_t>(1, std::min<int64_t>(ctx->num_sms / blocks, max_len / 256));
 }
 
+// MXFP4 calls whose sequences have kExpandBlocks row blocks or more first expand the attended
+// tokens to bf16 in the workspace (kv_expand_kernel) if that takes at most kExpandBytes; with
+// fewer blocks every block turns them on its own (kMx).
+constexpr int kExpandBlocks = 4;
+constexpr size_t kExpandBytes = (size_t)1 << 30;
+
+struct Expansion {
+  int64_t room;            // tokens per (sequence, KV head), whole tiles
+  size_t table, half, all; // bytes of the page table, of the keys as of the values, of all; 0: none
+};
+Expansion expansion(const tq_ctx* ctx, int batch, int G, int hkv, int64_t max_len, int64_t max_q) {
+  Expansion x{};
+  const int rows = block_rows(ctx->shape.d);
+  if ((max_q * G + rows - 1) / rows < kExpandBlocks) return x;
+  x.room = (max_len + 127) / 128 * 128;
+  const __int128 half = (__int128)batch * hkv * x.room * ctx->shape.d * 2;
+  if (half * 2 > (__int128)kExpandBytes) return x;
+  x.table = ((size_t)batch * hkv * sizeof(int32_t) + 127) / 128 * 128;
+  x.half = (size_t)half;
+  x.all = x.table + 2 * x.half;
+  return x;
+}
+
 }  // namespace
 
-size_t kv_prefill_workspace(const tq_ctx* ctx, int64_t total_q, int batch, int hq, int hkv, int64_t max_len,
-                            int64_t max_q) {
+size_t kv_prefill_workspace(const tq_ctx* ctx, int format, int64_t total_q, int batch, int hq, int hkv,
+                            int64_t max_len, int64_t max_q) {
   const int s = split_count(ctx, batch, hq / hkv, hkv, max_len, max_q);
-  return s > 1 ? (size_t)s * total_q * hq * (ctx->shape.d + 4) * sizeof(float) : 0;
+  const size_t parts = s > 1 ? (size_t)s * total_q * hq * (ctx->shape.d + 4) * sizeof(float) : 0;
+  const bool mx = format == TQ_KV_MXFP4;
+  return parts + (mx ? expansion(ctx, batch, hq / hkv, hkv, max_len, max_q).all : 0);
 }
 
 cudaError_t launch_kv_prefill(const tq_ctx* ctx, const PageView& pg, int format, const void* q, int64_t q_stride,
@@ -968,7 +1053,26 @@ cudaError_t launch_kv_prefill(const tq_ctx* ctx, const PageView& pg, int format,
   const int rows = block_rows(ctx->shape.d);
   a.blocks = (int)((max_q * a.G + rows - 1) / rows);
   const int d = ctx->shape.d;
-  if (format == TQ_KV_MXFP4) return pick_d<__nv_bfloat16, kMx>(d, a, ctx->device, stream);
+  if (format == TQ_KV_MXFP4) {
+    const Expansion x = expansion(ctx, batch, a.G, pg.hkv, max_len, max_q);
+    if (!x.all) return pick_d<__nv_bfloat16, kMx>(d, a, ctx->device, stream);
+    char* ws = static_cast<char*>(workspace);
+    ExpandArgs ea{a, ws + x.table, ws + x.table + x.half, reinterpret_cast<int32_t*>(ws), x.room};
+    const dim3 grid((unsigned)((max_len + kExpandTokens - 1) / kExpandTokens), (unsigned)(batch * pg.hkv));
+    if (d == 64) kv_expand_kernel<64><<<grid, 256, 0, stream>>>(ea);
+    else if (d == 128) kv_expand_kernel<128><<<grid, 256, 0, stream>>>(ea);
+    else kv_expand_kernel<256><<<grid, 256, 0, stream>>>(ea);
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    // the expanded tokens as a cache of one page per (sequence, KV head)
+    a.pg.k = ea.k, a.pg.v = ea.v;
+    a.pg.page_size = x.room, a.pg.n_pages = (int64_t)batch * pg.hkv, a.pg.n_slots = a.pg.n_pages * x.room;
+    a.pg.page_shift = -1, a.pg.per_head = 1;
+    a.pg.tok_b = d * 2, a.pg.page_b = x.room * d * 2, a.pg.head_b = 0;
+    a.table = ea.table, a.max_pages = 1;
+    a.part = reinterpret_cast<float*>(ws + x.all);
+    return pick<__nv_bfloat16>(d, a, ctx->device, stream);
+  }
   if (format == TQ_KV_BF16) return pick<__nv_bfloat16>(d, a, ctx->device, stream);
   return pick<__half>(d, a, ctx->device, stream);
 }

@@ -70,6 +70,10 @@ CASES = [
     ("mxfp4", 128, 2, 1, [(140, 1111)], 512, True, "nhd", 200),
     ("mxfp4", 64, 4, 2, [(77, 200), (1, 1)], 5, False, "hnd", 0),
     ("mxfp4", 256, 3, 1, [(50, 260)], 16, False, "nhd", 0),
+    ("mxfp4", 128, 8, 2, [(140, 300), (3, 50), (0, 7), (129, 129)], 16, False, "nhd", 0),  # expanded first
+    ("mxfp4", 64, 4, 1, [(300, 500), (1, 1)], 7, False, "gap", 150),
+    ("mxfp4", 256, 4, 2, [(130, 400)], 64, True, "nhd", 0),
+    ("mxfp4", 128, 64, 1, [(20, 3000), (9, 5)], 48, False, "hnd", 700),
     ("bf16", 128, 4, 1, [(5, 2), (3, 0), (200, 150)], 16, False, "nhd", 0),      # rows before the first token
     ("bf16", 128, 16, 1, [(16, 9000)], 16, False, "nhd", 0),                     # tokens split over CTAs
     ("f16", 64, 2, 1, [(3, 5000), (1, 1), (2, 4097)], 16, False, "nhd", 3000),
@@ -119,11 +123,12 @@ def simple(rng, fmt, d, g, hkv, lens, page=16, extra=1, max_len=None):
     return q_lens, kv_lens, cache, table, cu, q
 
 
-@pytest.mark.parametrize("fmt,d", [("bf16", 128), ("f16", 64), ("bf16", 256), ("mxfp4", 128)])
-def test_prefill_nonfinite_values_reach_only_rows_that_see_them(fmt, d):
+@pytest.mark.parametrize("fmt,d,g", [("bf16", 128, 2), ("f16", 64, 2), ("bf16", 256, 2), ("mxfp4", 128, 2),
+                                     ("mxfp4", 128, 8)])
+def test_prefill_nonfinite_values_reach_only_rows_that_see_them(fmt, d, g):
     """Infinities and NaN in keys and values of single tokens (on the diagonal, at the window's
     edge, in the middle), and a NaN query: every other row keeps its bits."""
-    g, hkv, window = 2, 2, 150
+    hkv, window = 2, 150
     rng = np.random.default_rng(11)
     ctx = make_ctx(d)
     q_lens, kv_lens, cache, table, cu, q = simple(rng, fmt, d, g, hkv, [(200, 500), (90, 90)])

@@ -132,4 +132,4 @@ def test_prefill_bad_caches_and_nothing_to_do():
     assert prefill(None) == EINVAL
     for kw in (dict(batch=0), dict(total=0), dict(max_q=0)):
         assert prefill(None, q=None, **kw) == OK
-    assert lib.tq_prefill_kv_pages_workspace_bytes(None, 1, 1, 4, 2, 10, 1) == 0
+    assert lib.tq_prefill_kv_pages_workspace_bytes(None, _lib.TQ_KV_BF16, 1, 1, 4, 2, 10, 1) == 0
