@@ -123,16 +123,16 @@ def simple(rng, fmt, d, g, hkv, lens, page=16, extra=1, max_len=None):
     return q_lens, kv_lens, cache, table, cu, q
 
 
-@pytest.mark.parametrize("fmt,d,g", [("bf16", 128, 2), ("f16", 64, 2), ("bf16", 256, 2), ("mxfp4", 128, 2),
-                                     ("mxfp4", 128, 8)])
-def test_prefill_nonfinite_values_reach_only_rows_that_see_them(fmt, d, g):
+@pytest.mark.parametrize("fmt,d,g,max_len", [("bf16", 128, 2, 500), ("f16", 64, 2, 500), ("bf16", 256, 2, 500),
+                                             ("mxfp4", 128, 2, 500), ("mxfp4", 128, 8, 500), ("mxfp4", 128, 4, 1 << 21)])
+def test_prefill_nonfinite_values_reach_only_rows_that_see_them(fmt, d, g, max_len):
     """Infinities and NaN in keys and values of single tokens (on the diagonal, at the window's
     edge, in the middle), and a NaN query: every other row keeps its bits."""
     hkv, window = 2, 150
     rng = np.random.default_rng(11)
     ctx = make_ctx(d)
-    q_lens, kv_lens, cache, table, cu, q = simple(rng, fmt, d, g, hkv, [(200, 500), (90, 90)])
-    args = (hkv, up(table), 500, up(cu), 200)
+    q_lens, kv_lens, cache, table, cu, q = simple(rng, fmt, d, g, hkv, [(200, 500), (90, 90)], max_len=max_len)
+    args = (hkv, up(table), max_len, up(cu), 200)
     kw = dict(seq_lens=up(kv_lens.astype(np.int32)), window=window)
     ref, rl = T.tq_prefill_kv_pages(ctx, q, T.KVPages(*cache), *args, **kw)
     base = [None if t is None else t.clone() for t in cache]
@@ -213,6 +213,22 @@ def test_prefill_window_reads_no_entry_before_it(fmt, page, window):
                                      seq_lens=up(kv_lens.astype(np.int32)), window=window)
     T.tq_check_device(ctx)
     check(cache, table, q_lens, kv_lens, cu, q, out, lse, page, False, hkv, window, fmt)
+
+
+@pytest.mark.parametrize("d,g,hkv,page,window", [(128, 8, 2, 16, 0), (64, 8, 4, 5, 0), (256, 3, 1, 48, 90)])
+def test_prefill_mxfp4_too_long_to_expand(d, g, hkv, page, window):
+    """Several row blocks over MXFP4 pages where the call's longest sequence allows no workspace for
+    all its tokens as bf16: each block turns the records itself."""
+    rng = np.random.default_rng(19)
+    ctx = make_ctx(d)
+    max_len = (1 << 21) + 5
+    lens = [(150, 700), (1, 1), (97, 97), (30, 20)]
+    q_lens, kv_lens, cache, table, cu, q = simple(rng, "mxfp4", d, g, hkv, lens, page=page, max_len=max_len)
+    assert T.tq_prefill_kv_pages_workspace_bytes(ctx, len(q), 4, hkv * g, hkv, max_len, 150) < 1 << 28
+    out, lse = T.tq_prefill_kv_pages(ctx, q, T.KVPages(*cache), hkv, up(table), max_len, up(cu), 150,
+                                     seq_lens=up(kv_lens.astype(np.int32)), window=window)
+    T.tq_check_device(ctx)
+    check(cache, table, q_lens, kv_lens, cu, q, out, lse, page, False, hkv, window, "mxfp4")
 
 
 def test_prefill_one_row_equals_decode():
