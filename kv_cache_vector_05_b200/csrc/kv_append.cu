@@ -235,80 +235,81 @@ struct ReadArgs {
   int64_t n;
   char* k_out;
   char* v_out;
-  int splits, iters;  // warps per token, groups of 32 / LPV heads per warp
+  int groups, per;    // groups of heads per token, groups per warp
+  int wide;           // outputs are 32-byte aligned
   unsigned int* err;
 };
 
-// A warp reads groups of VP heads of one token, LPV lanes a vector, kReads groups in flight;
-// blockIdx.y 0: keys, 1: values (or the one output asked for).
+// A group is VP heads of one token, LPV lanes a vector. A warp reads `per` consecutive groups, up to
+// kReads, all in flight (first their slots, then their records): what a group costs is the latency
+// of those two loads. blockIdx.y 0: keys, 1: values (or the one output asked for). A lane moves 16
+// bytes of a 16-bit record, or 8 bytes of codes, whose 16 coordinates it writes as one 32-byte line.
 constexpr int kReads = 4;
-template <bool MX, int LPV>
+template <bool MX, int HD>
 __global__ void __launch_bounds__(kThreads) read_kernel(const ReadArgs a) {
-  constexpr int VP = 32 / LPV;
+  constexpr int LPV = MX ? HD / 16 : HD / 8, VP = 32 / LPV, kIn = MX ? 8 : 16, kOut = MX ? 32 : 16;
   const PageView& pg = a.pg;
   const bool keys = a.k_out && (blockIdx.y == 0);
   const char* base = keys ? pg.k : pg.v;
   const uint8_t* sbase = keys ? pg.ks : pg.vs;
+  char* out = keys ? a.k_out : a.v_out;
   const int lane = threadIdx.x & 31, ch = lane % LPV;
-  const int64_t wid = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
-  const int64_t tok = quotient(wid, a.splits);
-  if (tok >= a.n) return;
-  const int split = (int)(wid - tok * a.splits);
-  char* out = (keys ? a.k_out : a.v_out) + tok * pg.hkv * (LPV * 16) + ch * 16;
-  const int64_t* slots = a.slot + (pg.per_head ? tok * pg.hkv : tok);
-  const int h0 = split * a.iters * VP, h1 = min(pg.hkv, h0 + a.iters * VP);
-  int64_t off0 = 0, soff0 = 0;
-  if (!pg.per_head) {
-    const int64_t slot = __ldg(slots);
-    if (slot < 0 || slot >= pg.n_slots) {
-      if (slot != -1 && lane == 0) atomicOr(a.err, kErrIndex);
-      return;
-    }
-    off0 = record_offset<MX>(pg, slot, soff0);
+  const int64_t first = ((int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5)) * a.per;
+  int64_t vec[kReads], slot[kReads];  // token * hkv + head, and its cache row (-1: nothing to read)
+  int head[kReads];
+#pragma unroll
+  for (int u = 0; u < kReads; ++u) {
+    const int64_t tok = quotient(first + u, a.groups);
+    head[u] = (int)(first + u - tok * a.groups) * VP + lane / LPV;
+    vec[u] = tok * pg.hkv + head[u];
+    const bool ok = u < a.per && tok < a.n && head[u] < pg.hkv;
+    slot[u] = ok ? __ldg(a.slot + (pg.per_head ? vec[u] : tok)) : -1;
   }
-  for (int hb = h0 + lane / LPV; hb < h1; hb += kReads * VP) {
-    uint4 x[kReads];
-    uint32_t sc[kReads];
-    bool ok[kReads];
+  uint4 x[kReads];
+  uint32_t sc[kReads];
 #pragma unroll
-    for (int u = 0; u < kReads; ++u) {
-      const int h = hb + u * VP;
-      ok[u] = h < h1;
-      if (!ok[u]) continue;
-      int64_t off, soff;
-      if (!pg.per_head) {
-        off = off0 + times(h, pg.head_b), soff = soff0 + times(h, pg.shead_b);
-      } else {
-        const int64_t slot = __ldg(slots + h);
-        ok[u] = slot >= 0 && slot < pg.n_slots;
-        if (!ok[u]) {
-          if (slot != -1 && ch == 0) atomicOr(a.err, kErrIndex);
-          continue;
-        }
-        off = record_offset<MX>(pg, slot, soff);
-      }
-      if constexpr (MX) {
-        x[u].x = *reinterpret_cast<const uint32_t*>(base + off + ch * 4);
-        sc[u] = sbase[soff + ch / 4];
-      } else {
-        x[u] = *reinterpret_cast<const uint4*>(base + off + ch * 16);
-      }
+  for (int u = 0; u < kReads; ++u) {
+    if (slot[u] < 0 || slot[u] >= pg.n_slots) {
+      if (slot[u] != -1 && ch == 0) atomicOr(a.err, kErrIndex);
+      slot[u] = -1;
+      continue;
     }
+    int64_t soff, off = record_offset<MX>(pg, slot[u], soff) + times(head[u], pg.head_b);
+    if constexpr (MX) {
+      const uint2 w = *reinterpret_cast<const uint2*>(base + off + ch * kIn);
+      x[u].x = w.x, x[u].y = w.y;
+      sc[u] = sbase[soff + times(head[u], pg.shead_b) + ch / 2];
+    } else {
+      x[u] = *reinterpret_cast<const uint4*>(base + off + ch * kIn);
+    }
+  }
 #pragma unroll
-    for (int u = 0; u < kReads; ++u) {
-      if (!ok[u]) continue;
-      if constexpr (MX) {
-        uint32_t h[4], r[4];
-        e2m1x8_f16(x[u].x, h);
-        const float f = e8m0(sc[u]);
+  for (int u = 0; u < kReads; ++u) {
+    if (slot[u] < 0) continue;
+    char* dst = out + vec[u] * (HD * 2) + ch * kOut;
+    if constexpr (MX) {
+      const float f = e8m0(sc[u]);
+      uint32_t r[8];
+#pragma unroll
+      for (int w = 0; w < 2; ++w) {
+        uint32_t h[4];
+        e2m1x8_f16(w ? x[u].y : x[u].x, h);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const float2 t = sm100::mul2(Half2<__half>::unpack(h[i]), make_float2(f, f));
-          r[i] = Half2<__nv_bfloat16>::pack(t.x, t.y);
+          r[4 * w + i] = Half2<__nv_bfloat16>::pack(t.x, t.y);
         }
-        x[u] = make_uint4(r[0], r[1], r[2], r[3]);
       }
-      *reinterpret_cast<uint4*>(out + (int64_t)(hb + u * VP) * (LPV * 16)) = x[u];
+      if (a.wide)
+        asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(dst), "r"(r[0]), "r"(r[1]), "r"(r[2]),
+                     "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                     : "memory");
+      else
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          reinterpret_cast<uint4*>(dst)[i] = make_uint4(r[4 * i], r[4 * i + 1], r[4 * i + 2], r[4 * i + 3]);
+    } else {
+      *reinterpret_cast<uint4*>(dst) = x[u];
     }
   }
 }
@@ -362,20 +363,20 @@ cudaError_t launch_kv_append(const tq_ctx* ctx, const PageView& pg, int format, 
 
 cudaError_t launch_kv_read(const tq_ctx* ctx, const PageView& pg, int format, int64_t n, const int64_t* slot,
                            void* k_out, void* v_out, cudaStream_t stream) {
-  ReadArgs a{pg, slot, n, static_cast<char*>(k_out), static_cast<char*>(v_out), 1, 1, ctx->d_err};
-  const int lpv = ctx->shape.d / 8, vp = 32 / lpv, groups = (pg.hkv + vp - 1) / vp;
+  ReadArgs a{pg, slot, n, static_cast<char*>(k_out), static_cast<char*>(v_out), 1, 1, 0, ctx->d_err};
+  a.wide = ((reinterpret_cast<uintptr_t>(k_out) | reinterpret_cast<uintptr_t>(v_out)) & 31) == 0;
+  const bool mx = format == TQ_KV_MXFP4;
+  const int d = ctx->shape.d, vp = 32 / (mx ? d / 16 : d / 8), groups = (pg.hkv + vp - 1) / vp;
   // one group per warp until the SMs hold 32 warps each, then up to the kReads in flight
   const int64_t want = (int64_t)ctx->num_sms * 32;
-  const int most = (int)std::max<int64_t>(1, std::min<int64_t>(kReads, n * groups / want));
-  a.splits = (groups + most - 1) / most;
-  a.iters = (groups + a.splits - 1) / a.splits;
-  const int64_t blocks = (n * a.splits + kThreads / 32 - 1) / (kThreads / 32);
+  a.groups = groups;
+  a.per = (int)std::max<int64_t>(1, std::min<int64_t>(kReads, n * groups / want));
+  const int64_t blocks = ((n * groups + a.per - 1) / a.per + kThreads / 32 - 1) / (kThreads / 32);
   if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
   const dim3 grid((unsigned)blocks, k_out && v_out ? 2 : 1);
-  const bool mx = format == TQ_KV_MXFP4;
-  if (lpv == 8) (mx ? read_kernel<true, 8> : read_kernel<false, 8>)<<<grid, kThreads, 0, stream>>>(a);
-  else if (lpv == 16) (mx ? read_kernel<true, 16> : read_kernel<false, 16>)<<<grid, kThreads, 0, stream>>>(a);
-  else (mx ? read_kernel<true, 32> : read_kernel<false, 32>)<<<grid, kThreads, 0, stream>>>(a);
+  if (d == 64) (mx ? read_kernel<true, 64> : read_kernel<false, 64>)<<<grid, kThreads, 0, stream>>>(a);
+  else if (d == 128) (mx ? read_kernel<true, 128> : read_kernel<false, 128>)<<<grid, kThreads, 0, stream>>>(a);
+  else (mx ? read_kernel<true, 256> : read_kernel<false, 256>)<<<grid, kThreads, 0, stream>>>(a);
   return cudaGetLastError();
 }
 
