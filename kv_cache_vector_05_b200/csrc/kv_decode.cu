@@ -14,7 +14,11 @@
 // __syncwarp alone, and keeps the running maximum, sum and output of its heads in registers.
 // A unit that one warp finishes is written out directly. The pieces of a unit that several
 // warps of a CTA share are merged through shared memory, the pieces of several CTAs by
-// combine_kernel, both in a fixed order: results do not depend on timing.
+// kv_combine_kernel, both in a fixed order: results do not depend on timing.
+//
+// A call of few units and short sequences is bound by its launches: there each unit gets a cluster
+// of up to 8 CTAs, which split its tiles and merge their pieces through each other's shared memory,
+// and the second launch is left out.
 //
 // Tensor cores (mma.sync m16n8k16): S^T = K Q^T with the 16 tokens as rows and the heads as 8
 // columns, O^T = V^T P^T with 16 value coordinates as rows. A product's inner index may be
@@ -70,6 +74,7 @@ struct DecArgs {
   char* out;
   int out_f32;
   float* lse;
+  int cluster;   // CTAs per unit, or 0: all tiles are split over the grid
   float* head;   // [warps][GB][HD + 4]: pieces a warp leaves at its first unit's end
   float* part;   // [2 CTAs][GB][HD + 4]: slot 2k CTA k's piece from its range's start, 2k + 1 a later one
   int4* meta;    // [CTAs]: {sequence, unit of it, last CTA, 1} of a unit begun in this CTA and shared
@@ -753,6 +758,21 @@ __device__ __forceinline__ void store4(const DecArgs& a, bool f16, int64_t at, f
   }
 }
 
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release; barrier.cluster.wait.acquire;" ::: "memory");
+}
+// Shared-memory address `a` of the cluster's CTA `rank`.
+__device__ __forceinline__ uint32_t peer_smem(uint32_t a, int rank) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ float4 peer_load4(uint32_t a) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(a) : "memory");
+  return v;
+}
+
 // x / n for x >= 0, n > 0, in 32 bits where they suffice (a 64-bit division is several hundred
 // cycles on the way to the first load).
 __device__ __forceinline__ int64_t divided(int64_t x, int64_t n) {
@@ -793,7 +813,13 @@ __global__ void __launch_bounds__(Config<FMT, HD>::kWarps * 32, 1) kv_decode_ker
     n = (int)(want < gridDim.x ? want : gridDim.x);
     cta0 = n ? scaled(total, k, n) : 0;
   };
-  if (a.batch <= NT) {  // one scan gives both
+  if (a.cluster) {  // this CTA's share of its unit
+    const int unit = k / a.cluster, b = unit / upb;
+    if (tid == 0) s_b = b, s_start = unit - b * upb;
+    total = extent<C::kTile>(a, b).nt;
+    n = a.cluster;
+    cta0 = 0;
+  } else if (a.batch <= NT) {  // one scan gives both
     const int64_t mine = tid < a.batch ? extent<C::kTile>(a, tid).nt : 0;
     const int64_t incl = warp_incl_scan(mine, lane);
     if (lane == 31) s_scan[w] = incl;
@@ -840,21 +866,22 @@ __global__ void __launch_bounds__(Config<FMT, HD>::kWarps * 32, 1) kv_decode_ker
       }
     }
   }
-  if (tid == 0) a.meta[k] = make_int4(0, 0, 0, 0);
+  if (tid == 0 && !a.cluster) a.meta[k] = make_int4(0, 0, 0, 0);
   __syncthreads();
 
-  const int64_t nw = (int64_t)n * W, gw = (int64_t)k * W + w;
-  const int64_t r0 = k < n ? scaled(total, gw, nw) : 0, r1 = k < n ? scaled(total, gw + 1, nw) : 0;
+  const int rank = a.cluster ? k % a.cluster : k;
+  const int64_t nw = (int64_t)n * W, gw = (int64_t)rank * W + w;
+  const int64_t r0 = rank < n ? scaled(total, gw, nw) : 0, r1 = rank < n ? scaled(total, gw + 1, nw) : 0;
   if (lane < 2) s_pb[2 * w + lane] = -1;
   Worker<T, FMT, HD, SMALL, WHOLE> wk(a, smem_u32(smem) + w * C::kRing, lane);
   Cursor ld{}, cur{};
   int seg_from = 0;
   bool open = false;
   if (r0 < r1) {
-    int64_t start = s_start;
+    int64_t start = a.cluster ? -s_start * total : s_start;  // unit 0's first tile in the ranges' order
     cur.b = s_b;
     cur.e = extent<C::kTile>(a, cur.b);
-    while (r0 >= start + (int64_t)cur.e.nt * upb) {
+    while (!a.cluster && r0 >= start + (int64_t)cur.e.nt * upb) {
       start += (int64_t)cur.e.nt * upb;
       cur.e = extent<C::kTile>(a, ++cur.b);
     }
@@ -891,7 +918,7 @@ __global__ void __launch_bounds__(Config<FMT, HD>::kWarps * 32, 1) kv_decode_ker
       if (++st == C::kStages) st = 0;
       if (cur.tile + 1 == cur.e.nt) {  // the unit's last tile
         wk.finish();
-        if (seg_from == 0) {
+        if (seg_from == 0 && !a.cluster) {
           wk.write_out(cur);
         } else if (i + 1 < r1) {       // begun by another warp: leave the piece for the merge
           wk.write_piece(a.head + gw * a.GB * kRow, min(a.GB, a.G - cur.hb * a.GB));
@@ -900,7 +927,7 @@ __global__ void __launch_bounds__(Config<FMT, HD>::kWarps * 32, 1) kv_decode_ker
             s_nt[2 * w] = cur.e.nt, s_tile0[2 * w] = r0;
           }
         }
-        open = seg_from != 0 && i + 1 == r1;
+        open = (seg_from != 0 || a.cluster) && i + 1 == r1;
         if (i + 1 < r1) {
           cur.tile = 0;
           wk.next_unit(cur);
@@ -937,9 +964,10 @@ __global__ void __launch_bounds__(Config<FMT, HD>::kWarps * 32, 1) kv_decode_ker
     todo &= ~run;
     const int last = 31 - __clz(run), kvh = a.HB == 1 ? uk : uk / a.HB, hb = uk - kvh * a.HB;
     const int heads = min(a.GB, a.G - hb * a.GB);
-    const bool whole = s_from[i] == 0 && s_to[last] == s_nt[i];
+    const bool whole = !a.cluster && s_from[i] == 0 && s_to[last] == s_nt[i];
     const int64_t row0 = (int64_t)b * a.hq + kvh * a.G + hb * a.GB;
-    float* part = a.part + (int64_t)(2 * k + (s_tile0[i] == cta0 ? 0 : 1)) * a.GB * kRow;
+    float* part = a.cluster ? pieces + W * a.GB * kRow
+                            : a.part + (int64_t)(2 * k + (s_tile0[i] == cta0 ? 0 : 1)) * a.GB * kRow;
     for (int x = tid; x < heads * (HD / 4); x += NT) {
       const int h = x / (HD / 4), d0 = (x % (HD / 4)) * 4;
       auto piece = [&](int j) {
@@ -971,10 +999,50 @@ __global__ void __launch_bounds__(Config<FMT, HD>::kWarps * 32, 1) kv_decode_ker
         if (d0 == 0) *reinterpret_cast<float2*>(part + h * kRow + HD) = make_float2(mx, ls);
       }
     }
-    if (!whole && s_from[i] == 0 && tid == 0) {  // begun here, ended by a later CTA
+    if (!whole && !a.cluster && s_from[i] == 0 && tid == 0) {  // begun here, ended by a later CTA
       const int64_t end = s_tile0[i] + s_nt[i];
       a.meta[k] = make_int4(b, uk, (int)divided(end * n - 1, total), 1 + (s_tile0[i] == cta0 ? 0 : 1));
     }
+  }
+
+  if (a.cluster) {  // the unit's rows from its CTAs' pieces, each CTA a share of the heads
+    float* mine = pieces + W * a.GB * kRow;
+    if (!__syncthreads_or(pb >= 0))  // no tile here
+      for (int x = tid; x < a.GB * kRow; x += NT) mine[x] = x % kRow == HD ? kNegHuge : 0.f;
+    if (a.cluster > 1) cluster_sync();
+    else __syncthreads();
+    const int unit = k / a.cluster, b = unit / upb, uk = unit - b * upb;
+    const int kvh = a.HB == 1 ? uk : uk / a.HB, hb = uk - kvh * a.HB;
+    const int heads = min(a.GB, a.G - hb * a.GB);
+    const int64_t row0 = (int64_t)b * a.hq + kvh * a.G + hb * a.GB;
+    for (int x = tid; x < (heads - rank + a.cluster - 1) / a.cluster * (HD / 4); x += NT) {
+      const int h = rank + x / (HD / 4) * a.cluster, d0 = (x % (HD / 4)) * 4;
+      const uint32_t at = smem_u32(mine + h * kRow);
+      float4 ml[8], v[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        ml[j] = make_float4(kNegHuge, 0.f, 0.f, 0.f), v[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (j >= a.cluster) continue;
+        const uint32_t p = a.cluster > 1 ? peer_smem(at, j) : at;
+        ml[j] = peer_load4(p + HD * 4), v[j] = peer_load4(p + d0 * 4);
+      }
+      float mx = kNegHuge, ls = 0.f;
+      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) mx = fmaxf(mx, ml[j].x);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float f = ex2(ml[j].x - mx);
+        ls = fmaf(f, ml[j].y, ls);
+        o.x = fmaf(f, v[j].x, o.x), o.y = fmaf(f, v[j].y, o.y), o.z = fmaf(f, v[j].z, o.z), o.w = fmaf(f, v[j].w, o.w);
+      }
+      const float inv = ls == 0.f ? 0.f : 1.f / ls;
+      store4(a, std::is_same<T, __half>::value, (row0 + h) * HD + d0,
+             make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv));
+      if (a.lse && d0 == 0) a.lse[row0 + h] = (mx + log2f(ls)) * kLn2;
+    }
+    if (a.cluster > 1) cluster_sync();  // no CTA leaves while another reads its shared memory
+    return;
   }
 
   // sequences without tokens: zero rows
@@ -1060,13 +1128,24 @@ cudaError_t run(const DecArgs& a, int device, int ctas, cudaStream_t st) {
     if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem)) != cudaSuccess) return e;
     if (device < 64) configured.fetch_or((uint64_t)1 << device);
   }
+  cudaLaunchConfig_t cfg{};
+  cudaLaunchAttribute at{};
+  if (a.cluster) {
+    cfg.gridDim = dim3(a.batch * a.pg.hkv * a.HB * a.cluster);
+    cfg.blockDim = dim3(C::kWarps * 32);
+    cfg.dynamicSmemBytes = C::kSmem;
+    cfg.stream = st;
+    at.id = cudaLaunchAttributeClusterDimension;
+    at.val.clusterDim.x = a.cluster, at.val.clusterDim.y = at.val.clusterDim.z = 1;
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, a);
+  }
   kern<<<ctas, C::kWarps * 32, C::kSmem, st>>>(a);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(ctas, a.GB);
   cfg.blockDim = dim3(256);
   cfg.stream = st;
-  cudaLaunchAttribute at{};
   at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &at;
@@ -1089,6 +1168,18 @@ cudaError_t pick_d(int d, const DecArgs& a, int device, int ctas, cudaStream_t s
 }
 
 constexpr int kMostWarps = 16;
+// CTAs per unit of a call whose units all run at once that way, or 0: the grid's even split. Clusters
+// of 8, 4 and 2 CTAs find room for 8, 32 and 64 units on the chip's groups of SMs (16 clusters of 8
+// already take two rounds). A unit's own CTAs save the second launch but share out nothing between
+// units of different lengths, so they are kept to few tokens each. In a graph, clusters against the
+// even split, equal lengths, d = 128, 4 heads on 1, bf16: 4 units of 1000 tokens 8.0 / 9.9 us, of
+// 2000 9.3 / 9.9, of 4000 11.5 / 10.9; 32 units of 1000 9.6 / 12.5, of 2000 12.2 / 13.4, of 4000 16.9 /
+// 17.6; 128 units of 100 7.2 / 13.8, of 512 11.2 / 14.2.
+int cluster_size(const tq_ctx* ctx, int64_t units, int64_t len) {
+  const int c = units <= 8 ? 8 : units <= 32 ? 4 : units <= 64 ? 2 : units <= ctx->num_sms ? 1 : 0;
+  const int64_t most = (c == 8 ? 256 : 512) / (ctx->shape.d == 256 ? 2 : 1);
+  return c && len <= most * c ? c : 0;
+}
 
 }  // namespace
 
@@ -1112,6 +1203,7 @@ cudaError_t launch_kv_decode(const tq_ctx* ctx, const PageView& pg, int format, 
   a.window = window, a.scale_log2 = scale * 1.4426950408889634f;
   a.out = static_cast<char*>(out), a.out_f32 = out_f32, a.lse = lse, a.err = ctx->d_err;
   const int ctas = ctx->num_sms;
+  a.cluster = cluster_size(ctx, (int64_t)batch * pg.hkv * a.HB, window && window < max_len ? window : max_len);
   const size_t row = (size_t)a.GB * (ctx->shape.d + 4);
   a.meta = static_cast<int4*>(workspace);
   a.part = reinterpret_cast<float*>(a.meta + ctas);

@@ -126,6 +126,16 @@ CASES = [
     ("mxfp4", 256, 5, 1, EDGE, 33, False, "nhd", 40, "bf16"),
     ("bf16", 128, 2, 8, [100] * 130 + [0] * 20 + [999] * 7, 16, False, "nhd", 0, "f32"),  # units inside warps
     ("bf16", 64, 1, 1, list(range(0, 700)), 16, False, "nhd", 0, "f32"),                   # batch above a block
+    # long sequences: tiles split over the whole grid
+    ("bf16", 64, 17, 1, [0, 9000, 33, 1], 24, False, "nhd", 0, "f32"),
+    ("mxfp4", 64, 12, 2, [6000, 5, 0], 7, True, "nhd", 5001, "bf16"),
+    ("mxfp4", 256, 4, 1, [7000, 640], 32, False, "hnd", 0, "f32"),
+    ("f16", 256, 5, 1, [4100, 17, 2500], 16, False, "gap", 0, "f16"),
+    ("bf16", 256, 9, 1, [5000, 1], 33, True, "nhd", 4500, "f32"),
+    # one to eight CTAs per unit
+    ("bf16", 128, 4, 8, [1999, 0, 3], 16, False, "nhd", 0, "f32"),
+    ("bf16", 128, 4, 8, [400] * 9 + [0, 1, 17, 1000], 16, False, "nhd", 0, "bf16"),
+    ("f16", 64, 8, 16, [500, 512, 1, 0, 77, 300, 16, 15], 8, False, "nhd", 100, "f32"),
 ]
 
 
