@@ -452,7 +452,8 @@ size_t tq_decode_kv_pages_workspace_bytes(const tq_ctx* ctx, int batch, int hq, 
  *   max_len     at most max_pages * page_size, and below 2^31
  *   window      0, or the number of newest tokens attended
  *   softmax_scale  logit scale; 0 selects 1/sqrt(d)
- *   out         device [batch][hq][d] of out_dtype: TQ_F32 or q_dtype
+ *   out         device [batch][hq][d] of out_dtype: TQ_F32 or q_dtype; out and lse must not
+ *               overlap the inputs
  *   lse         NULL, or device fp32 [batch][hq]: log sum_t exp(logit_t) (natural log)
  * A sequence of length 0 gets a zero row and lse = -inf. Slots past a sequence's length or
  * before its window may hold anything, infinities and NaN included.

@@ -659,10 +659,13 @@ def _table(block_table, batch: int, hkv: int, pages: KVPages) -> int:
                   pages)
 
 
-def _workspace(workspace, need: int, pages: KVPages):
+def _workspace(workspace, need: int, pages: KVPages, stream):
     import torch
     if workspace is None:
-        return torch.empty(max(need, 256), dtype=torch.uint8, device=pages.device)
+        workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=pages.device)
+        if stream is not None:                                # freed on return, used on `stream`
+            workspace.record_stream(stream)
+        return workspace
     if workspace.get_device() != pages.index or not workspace.is_contiguous():
         raise ValueError(f"the workspace must be a contiguous tensor on {pages.device}")
     return workspace
@@ -691,7 +694,7 @@ def tq_decode_kv_pages(ctx: Context, q, pages: KVPages, hkv: int, block_table, m
     if lse is None:
         lse = torch.empty((batch, hq), dtype=torch.float32, device=q.device)
     need = lib.tq_decode_kv_pages_workspace_bytes(ctx.handle, batch, hq, hkv) if workspace is None else 0
-    workspace = _workspace(workspace, need, pages)
+    workspace = _workspace(workspace, need, pages, stream)
     status = lib.tq_decode_kv_pages(
         ctx.handle, p, q.data_ptr(), pages.code, qs, batch, hq, table, block_table.shape[-1], lens, max_len, window,
         softmax_scale, _index(out, "out", out.dtype, q.shape, pages), _dtype_code(out.dtype),
@@ -730,7 +733,7 @@ def tq_prefill_kv_pages(ctx: Context, q, pages: KVPages, hkv: int, block_table, 
     need = 0
     if workspace is None:
         need = tq_prefill_kv_pages_workspace_bytes(ctx, total_q, batch, hq, hkv, max_len, max_q, pages.format)
-    workspace = _workspace(workspace, need, pages)
+    workspace = _workspace(workspace, need, pages, stream)
     status = lib.tq_prefill_kv_pages(
         ctx.handle, p, q.data_ptr(), pages.code, qs, total_q, batch, hq, starts, max_q, table, block_table.shape[-1],
         lens, max_len, window, softmax_scale, _index(out, "out", q.dtype, q.shape, pages),

@@ -109,6 +109,7 @@ tq_status check_attention(const char* fn, const tq_kv_pages* p, const void* q, t
                 "q must be of a 16-bit cache's type (MXFP4: bf16)");
   if (hq < 1 || hq > 65535 || hq % p->hkv) return fail(TQ_EINVAL, fn, "hq must be a multiple of hkv in [1, 65535]");
   if (!q || !out) return fail(TQ_EINVAL, fn, "NULL q or out");
+  if (q == out) return fail(TQ_EINVAL, fn, "out must not be q");
   if (!aligned(out, 16)) return fail(TQ_EINVAL, fn, "out must be 16-byte aligned");
   if (!block_table) return fail(TQ_EINVAL, fn, "NULL block table");
   if (!aligned(block_table, 4) || !aligned(seq_lens, 4) || !aligned(lse, 4))

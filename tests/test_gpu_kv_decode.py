@@ -351,26 +351,31 @@ def test_decode_past_32_bit_offsets(fmt):
     check(small, table, lens, q, out, lse, page, False, hkv, 0, fmt, "f32")
 
 
-def test_decode_repeats_on_streams_and_in_graphs():
+@pytest.mark.parametrize("cut", [1, 10])     # tiles split over the grid; a cluster per unit
+def test_decode_repeats_on_streams_and_in_graphs(cut):
     """The same bits from every run, on another stream, captured and replayed with other lengths
     and queries, and from two graphs that share a workspace but run one after the other."""
     d, hkv, g, page, batch = 128, 2, 4, 16, 5
     rng = np.random.default_rng(8)
     ctx = make_ctx(d)
-    lens = np.array([3000, 17, 0, 801, 1600])
+    top = 3000 // cut
+    lens = np.array([top, 17, 0, 801 // cut, 1600 // cut])
     cache = random_cache(rng, "bf16", 400, page, hkv, d, False)
     table = up(block_tables(rng, lens, page, hkv, False, 188, 400))
     pages = T.KVPages(*cache)
     q = torch.randn((batch, hkv * g, d), device=DEV).to(torch.bfloat16)
     ln = up(lens.astype(np.int32))
-    ref, rl = T.tq_decode_kv_pages(ctx, q, pages, hkv, table, 3000, seq_lens=ln)
+    ref, rl = T.tq_decode_kv_pages(ctx, q, pages, hkv, table, top, seq_lens=ln)
     side = torch.cuda.Stream()
     side.wait_stream(torch.cuda.current_stream())
     for _ in range(3):
         with torch.cuda.stream(side):
-            out, lse = T.tq_decode_kv_pages(ctx, q, pages, hkv, table, 3000, seq_lens=ln)
+            out, lse = T.tq_decode_kv_pages(ctx, q, pages, hkv, table, top, seq_lens=ln)
         side.synchronize()
         assert torch.equal(out, ref) and torch.equal(lse, rl)
+    out, lse = T.tq_decode_kv_pages(ctx, q, pages, hkv, table, top, seq_lens=ln, stream=side)
+    side.synchronize()
+    assert torch.equal(out, ref) and torch.equal(lse, rl)
     ws = torch.empty(T.tq_decode_kv_pages_workspace_bytes(ctx, batch, hkv * g, hkv), dtype=torch.uint8, device=DEV)
     ws.fill_(255)
     graphs, outs = [], []
@@ -378,13 +383,13 @@ def test_decode_repeats_on_streams_and_in_graphs():
         gr = torch.cuda.CUDAGraph()
         o, ls = torch.empty_like(ref), torch.empty_like(rl)
         with torch.cuda.graph(gr):
-            T.tq_decode_kv_pages(ctx, q, pages, hkv, table, 3000, seq_lens=ln, out=o, lse=ls, workspace=ws)
+            T.tq_decode_kv_pages(ctx, q, pages, hkv, table, top, seq_lens=ln, out=o, lse=ls, workspace=ws)
         graphs.append(gr)
         outs.append((o, ls))
     for i in range(4):
         q.normal_()
-        ln.copy_(up(np.minimum(lens, [3000 - 7 * i, 17, i, 800, 1000 * i // 2]).astype(np.int32)))
-        want, wl = T.tq_decode_kv_pages(ctx, q, pages, hkv, table, 3000, seq_lens=ln)
+        ln.copy_(up(np.minimum(lens, [top - 7 * i, 17, i, 800, 1000 * i // 2]).astype(np.int32)))
+        want, wl = T.tq_decode_kv_pages(ctx, q, pages, hkv, table, top, seq_lens=ln)
         for gr, (o, ls) in zip(graphs, outs):
             gr.replay()
             torch.cuda.synchronize()

@@ -10,6 +10,7 @@ from kv_cache_vector_05_b200 import _lib  # noqa: E402
 lib, EINVAL, EUNSUP, OK = _lib.lib, _lib.TQ_EINVAL, _lib.TQ_EUNSUPPORTED, _lib.TQ_OK
 P = ctypes.c_void_p(1 << 20)                  # 16-byte aligned, never dereferenced
 ODD = ctypes.c_void_p((1 << 20) + 2)
+OUT = ctypes.c_void_p(1 << 21)
 
 
 def pages(**kw):
@@ -79,7 +80,7 @@ def test_read_refusals():
 
 
 def decode(pg, q=P, q_dtype=_lib.TQ_BF16, batch=2, hq=4, table=P, max_pages=4, lens=None, max_len=64, window=0,
-           scale=0.0, out=P, out_dtype=_lib.TQ_F32, lse=None, ws=P):
+           scale=0.0, out=OUT, out_dtype=_lib.TQ_F32, lse=None, ws=P):
     return lib.tq_decode_kv_pages(None, pg, q, q_dtype, hq * 128, batch, hq, table, max_pages, lens, max_len, window,
                                   scale, out, out_dtype, lse, ws, 1 << 20, None)
 
@@ -87,7 +88,7 @@ def decode(pg, q=P, q_dtype=_lib.TQ_BF16, batch=2, hq=4, table=P, max_pages=4, l
 ATTENTION = [
     (dict(q_dtype=_lib.TQ_F32), EUNSUP, "16-bit"), (dict(q_dtype=_lib.TQ_F16), EUNSUP, "16-bit"),
     (dict(hq=5), EINVAL, "hq"), (dict(hq=0), EINVAL, "hq"), (dict(q=None), EINVAL, "NULL q"),
-    (dict(out=None), EINVAL, "NULL q or out"), (dict(out=ODD), EINVAL, "out must be 16-byte"),
+    (dict(out=None), EINVAL, "NULL q or out"), (dict(out=P), EINVAL, "must not be q"), (dict(out=ODD), EINVAL, "out must be 16-byte"),
     (dict(table=None), EINVAL, "block table"), (dict(table=ODD), EINVAL, "4-byte"), (dict(lens=ODD), EINVAL, "4-byte"),
     (dict(lse=ODD), EINVAL, "4-byte"), (dict(max_len=-1), EINVAL, "max_len"),
     (dict(max_len=(1 << 31) - 1), EINVAL, "max_len"), (dict(max_len=65), EINVAL, "max_pages"),
@@ -113,7 +114,7 @@ def test_decode_bad_caches_and_empty_batch():
 
 
 def prefill(pg, q=P, q_dtype=_lib.TQ_BF16, total=10, batch=2, hq=4, cu=P, max_q=8, table=P, max_pages=4, lens=None,
-            max_len=64, window=0, scale=0.0, out=P, lse=None, ws=P):
+            max_len=64, window=0, scale=0.0, out=OUT, lse=None, ws=P):
     return lib.tq_prefill_kv_pages(None, pg, q, q_dtype, hq * 128, total, batch, hq, cu, max_q, table, max_pages, lens,
                                    max_len, window, scale, out, lse, ws, 1 << 20, None)
 
