@@ -542,10 +542,10 @@ class KVPages:
         if not self.per_head and hkv != self.hkv:
             raise ValueError(f"the page cache holds {self.hkv} KV heads, not {hkv}")
         p = self._struct
-        if p.hkv != hkv:
-            if p.hkv:                                         # a per-head cache used with another head count
-                p = tq_kv_pages.from_buffer_copy(p)
+        if p.hkv != hkv:                                      # a new one: a call of another thread may hold the old
+            p = tq_kv_pages.from_buffer_copy(p)
             p.hkv = hkv
+            self._struct = p
         return ctypes.byref(p)
 
 

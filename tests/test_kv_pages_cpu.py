@@ -134,3 +134,13 @@ def test_prefill_bad_caches_and_nothing_to_do():
     for kw in (dict(batch=0), dict(total=0), dict(max_q=0)):
         assert prefill(None, q=None, **kw) == OK
     assert lib.tq_prefill_kv_pages_workspace_bytes(None, _lib.TQ_KV_BF16, 1, 1, 4, 2, 10, 1) == 0
+
+
+def test_head_count_of_a_call_under_way_is_kept():
+    """Two threads may use one per-head cache with different head counts: each call has its own structure."""
+    cache = object.__new__(T.KVPages)
+    cache.d, cache.index, cache.per_head, cache._struct = 64, 0, True, _lib.tq_kv_pages()
+    ctx = type("Ctx", (), {"d": 64, "device": 0})
+    first, second, again = (cache.struct(ctx, hkv)._obj for hkv in (2, 5, 5))
+    assert (first.hkv, second.hkv) == (2, 5) and again is second
+    assert cache.struct(ctx, 2)._obj.hkv == 2 and second.hkv == 5
